@@ -537,6 +537,115 @@ GDN_API gdn_status gdn_chunk_prefill_layer(const void *q, const void *k, const v
                                            size_t workspace_bytes, gdn_stream_t stream);
 
 /*
+ * ---- Selective state space scan -------------------------------------------
+ * The additive sibling of the delta rule, with the same state layout: for every
+ * sequence n and value head h (reading group g = floor(h / (HV / HK)) of b and c)
+ *
+ *     delta_t = dt_t[h] + dt_bias[h], or softplus of it with GDN_SSM_SOFTPLUS
+ *     alpha_t = exp(delta_t * a[h])
+ *     S_t = alpha_t S_{t-1} + delta_t x_t b_t^T      y_t = S_t c_t + d[h] x_t
+ *
+ * a[h] <= 0 and delta_t >= 0 are expected (decays in [0, 1]); nothing checks them,
+ * and growing states may overflow.  Inputs have to be finite: a NaN or an infinity
+ * in a token of a sequence may reach every output of its 128-token chunk and all
+ * later ones (no other sequence, and nothing in rows behind the last sequence).
+ */
+#define GDN_SSM_SOFTPLUS 32u
+
+/*
+ * The scan over prompts.
+ *   x, y   [B][T][HV][dv] dtype       b, c  [B][T][HK][dk] dtype
+ *   dt     [B][T][HV] fp32            a, d, dt_bias [HV] fp32 (d, dt_bias may be NULL: 0)
+ *   h0, hT [N][HV][dv][dk] fp32 as in gdn_chunk_prefill (NULL: zero start / not
+ *          wanted; hT may alias h0), cu_seqlens, N, T and B as there.  Tokens behind
+ *          cu_seqlens[N] are neither read as inputs nor written.
+ * x_row, b_row, c_row: elements between a token's row of x (b, c) and the next
+ * token's, so that the three may be parts of one wider row (the convolved x | b | c
+ * row of gdn_short_conv); 0: dense.  y is dense.
+ * Supported: HV % HK == 0; dk, dv in {32, 64, 128}; GDN_BF16 or GDN_F32; fewer than
+ * 2^31 tokens.  States are fp32 throughout.  Alignment: x, b, c, y, h0, hT, workspace
+ * 16 bytes, the rows' byte strides multiples of 16.
+ * workspace: device scratch of gdn_ssm_prefill_workspace_size(...) bytes (may be NULL
+ * where that is 0), not to be shared by calls that may overlap; gdn_read_status as
+ * after gdn_chunk_prefill (where the size is not 0).
+ * N == 0: GDN_OK, nothing launched.  T == 0: hT gets h0 (or zero).
+ */
+GDN_API gdn_status gdn_ssm_prefill(const void *x, const void *b, const void *c, const float *dt,
+                                   const float *a, const float *d, const float *dt_bias,
+                                   const float *h0, const int32_t *cu_seqlens, int N, int64_t T,
+                                   int HK, int HV, int dk, int dv, int64_t x_row, int64_t b_row,
+                                   int64_t c_row, unsigned flags, gdn_dtype dtype, void *y,
+                                   float *hT, void *workspace, size_t workspace_bytes,
+                                   gdn_stream_t stream);
+
+/* Bytes of device workspace gdn_ssm_prefill needs (0 also for sizes it would reject). */
+GDN_API size_t gdn_ssm_prefill_workspace_size(int N, int64_t T, int HK, int HV, int dk, int dv,
+                                              gdn_dtype dtype, int varlen);
+
+/*
+ * One token of the rule for N sequences, with the short causal convolution of
+ * gdn_short_conv over the token's row in front of it (kept in fp32 between the two).
+ *   xbc [N][HV*dv + 2*HK*dk] dtype, a row x | b | c; rows xbc_row elements apart (0: dense)
+ *   conv_weight [C][conv_width] fp32, conv_bias [C] fp32 or NULL, conv_state and
+ *   conv_state_out [N][conv_width-1][C] dtype (C the row's width; the same buffer:
+ *   updated in place; otherwise they must not overlap).  conv_weight NULL: xbc is
+ *   already convolved and the other conv arguments are ignored.
+ *   dt [N][HV] fp32; a, d, dt_bias as above; state, state_out [N][HV][dv][dk] fp32
+ *   (the same buffer: in place; otherwise they must not overlap); y [N][HV][dv] dtype
+ * flags: GDN_SSM_SOFTPLUS, GDN_CONV_SILU.  Supported: dk in {32, 64, 128},
+ * 1 <= dv <= 256, widths as gdn_short_conv.  Alignment: states 16 bytes, the rest
+ * their element's size.  N == 0: GDN_OK, nothing launched.
+ */
+GDN_API gdn_status gdn_ssm_step(const void *xbc, const float *dt, const float *a, const float *d,
+                                const float *dt_bias, const float *conv_weight,
+                                const float *conv_bias, const void *conv_state,
+                                void *conv_state_out, int conv_width, const float *state,
+                                float *state_out, int N, int HK, int HV, int dk, int dv,
+                                int64_t xbc_row, unsigned flags, gdn_dtype dtype, void *y,
+                                gdn_stream_t stream);
+
+/*
+ * ---- Norms around a block --------------------------------------------------
+ * rms(u) = u / sqrt(mean(u^2) + eps); f(z) = sigmoid(z), or z sigmoid(z) with
+ * GDN_GATE_SILU; with GDN_NORM_UNIT_OFFSET the weights stand for 1 + weight.  Sums,
+ * statistics and products are fp32, rounded once to the output's type.
+ */
+#define GDN_GATE_SILU 64u
+#define GDN_NORM_GATE_FIRST 128u
+#define GDN_NORM_UNIT_OFFSET 256u
+
+/*
+ * Norm of the read-out with its gate, over groups of D elements (a head, or a row):
+ *   y = rms(o) w f(z), or with GDN_NORM_GATE_FIRST  y = rms(o f(z)) w
+ * o, z [rows][G][D] dtype, rows o_row, z_row elements apart (0: dense; z may be a part
+ * of a wider row); y dense, may be o where o is dense.  z NULL: no gate.  weight fp32
+ * [D] (weight_groups 1) or [G][D] (weight_groups G), or NULL (1).
+ * Supported: D <= 65536, fewer than 2^31 groups in all.  Alignment: the elements' size;
+ * rows of whole aligned 16-byte vectors run at memory speed, others element by element.
+ * rows == 0: GDN_OK, nothing launched.
+ */
+GDN_API gdn_status gdn_gated_norm(const void *o, const void *z, const float *weight, int64_t rows,
+                                  int G, int D, int64_t o_row, int64_t z_row, int weight_groups,
+                                  float eps, unsigned flags, gdn_dtype dtype, void *y,
+                                  gdn_stream_t stream);
+
+/*
+ * Between two blocks, in one pass over rows of C elements:
+ *   t = x, or rms(x) post_weight;  t = t f(z);  h = residual + scale t
+ *   residual_out = h,  y = rms(h) weight      (the norm of h before its rounding)
+ * x, z, y [rows][C] dtype; residual, residual_out [rows][C] residual_dtype (GDN_F32 or
+ * dtype); weight, post_weight [C] fp32.  NULL: post_weight no norm after the block, z no
+ * gate, residual zero, weight 1; y or residual_out (not both) not wanted.  y may be x,
+ * residual_out may be residual; other overlaps of outputs and inputs are not allowed.
+ * Supported: C <= 65536, rows < 2^31.  Alignment as gdn_gated_norm.
+ */
+GDN_API gdn_status gdn_residual_norm(const void *x, const void *residual, const float *weight,
+                                     const float *post_weight, const void *z, int64_t rows, int C,
+                                     float scale, float eps, unsigned flags, gdn_dtype dtype,
+                                     gdn_dtype residual_dtype, void *residual_out, void *y,
+                                     gdn_stream_t stream);
+
+/*
  * Reads the device status word a prefill call left in its workspace (HOST
  * call; synchronises `stream`).  Returns GDN_OK when every on-device wait of
  * the last call on this workspace completed, GDN_ERR_TIMEOUT when one gave up

@@ -153,4 +153,67 @@ size_t prefill_workspace_bytes(const PrefillArgs &a);
 // status word of the workspace-free prefill's library array (gdn_noalloc.cu)
 gdn_status noalloc_read_status(cudaStream_t stream);
 
+// ---- selective state space scan (gdn_ssm_*.cu) ----
+struct SsmArgs {
+    const void *x, *b, *c;            // [tokens][HV][dv], [tokens][HK][dk] x 2, rows x_row, b_row, c_row apart
+    const float *dt, *a, *d, *dt_bias;   // [tokens][HV], [HV] each (d, dt_bias may be null)
+    const float *h0;
+    const int32_t *cu_seqlens;
+    int N;
+    int64_t T;
+    int HK, HV, dk, dv;
+    int64_t x_row, b_row, c_row;      // elements between tokens
+    gdn_dtype dtype;
+    bool softplus;
+    void *y;
+    float *hT;
+    void *workspace;
+    size_t workspace_bytes;
+};
+struct SsmStepArgs {
+    const void *xbc;                  // [N][HV*dv + 2*HK*dk], rows xbc_row apart
+    const float *dt, *a, *d, *dt_bias;
+    const float *conv_w, *conv_b;     // null: xbc is already convolved
+    const void *conv_state;
+    void *conv_state_out;             // may be conv_state
+    int conv_width;
+    bool conv_silu, softplus;
+    const float *state;
+    float *state_out;                 // may be state
+    int N, HK, HV, dk, dv;
+    int64_t xbc_row;
+    gdn_dtype dtype;
+    void *y;
+};
+bool ssm_supported(int dk, int dv);
+size_t ssm_workspace_bytes(const SsmArgs &a);
+cudaError_t launch_ssm_prefill(const SsmArgs &a, cudaStream_t stream);
+cudaError_t launch_ssm_step(const SsmStepArgs &a, cudaStream_t stream);
+
+// ---- norms around a block (gdn_norm.cu) ----
+struct GatedNormArgs {
+    const void *o, *z;                // z may be null
+    const float *weight;              // [D] or [G][D], or null
+    int64_t rows, o_row, z_row;
+    int G, D;
+    bool weight_per_group, silu, gate_first, unit_offset;
+    float eps;
+    gdn_dtype dtype;
+    void *y;
+};
+struct ResidualNormArgs {
+    const void *x, *z;                // z may be null
+    const void *residual;             // may be null (zero)
+    const float *post_weight, *weight;   // null: no norm after the block; weight 1
+    int64_t rows;
+    int C;
+    bool silu, unit_offset;
+    float scale, eps;
+    gdn_dtype dtype, res_dtype;
+    void *residual_out, *y;           // either may be null
+};
+constexpr int kNormMaxWidth = 65536;
+cudaError_t launch_gated_norm(const GatedNormArgs &a, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormArgs &a, cudaStream_t stream);
+
 }  // namespace gdn

@@ -1,0 +1,62 @@
+// Shared pieces of the state space scan kernels (gdn_ssm_*.cu): the cut of the
+// sequences into segments, the step size and decay of a token, bf16 splitting.
+#pragma once
+
+#include "gdn_common.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace ssm {
+
+// The sequences are cut into segments of `seg_len` tokens (at least one per
+// sequence, also where it is empty), numbered through all sequences.  Without
+// cu_seqlens the map is arithmetic; with it plan_kernel writes the table.
+struct SegMap {
+    const int4 *table;      // [bound] {sequence, first token, tokens, index in sequence}, or null
+    const int *first;       // [N + 1] first segment of each sequence (with the table)
+    int N, nseg;            // sequences; segments per sequence (without the table)
+    int64_t T;              // tokens per sequence (without the table)
+    int seg_len;
+};
+
+struct Seg {
+    int n, idx, len;        // sequence, index in it, tokens
+    int64_t t0;             // first token (row of the packed batch)
+    bool ok, last;
+};
+
+__device__ __forceinline__ Seg find_seg(const SegMap &m, int s) {
+    Seg r;
+    if (m.table) {
+        r.ok = s < m.first[m.N];
+        if (!r.ok) return r;
+        const int4 e = m.table[s];
+        r.n = e.x;
+        r.t0 = e.y;
+        r.len = e.z;
+        r.idx = e.w;
+        r.last = s + 1 == m.first[r.n + 1];
+    } else {
+        r.ok = true;
+        r.n = s / m.nseg;
+        r.idx = s - r.n * m.nseg;
+        const int64_t at = (int64_t)r.idx * m.seg_len;
+        const int64_t left = m.T - at;
+        r.len = (int)(left < m.seg_len ? left : m.seg_len);
+        r.t0 = (int64_t)r.n * m.T + at;
+        r.last = r.idx + 1 == m.nseg;
+    }
+    return r;
+}
+
+// log(1 + e^x), finite and accurate at both ends
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+// step size of one token and head
+__device__ __forceinline__ float step_size(float dt, float bias, bool soft) {
+    const float v = dt + bias;
+    return soft ? softplus(v) : v;
+}
+
+}  // namespace ssm
+}  // namespace gdn

@@ -1,0 +1,415 @@
+// Selective state space scan on CUDA cores: fp32 calls and the head dims that
+// the tensor-core scan does not take.
+//
+//   delta_t = softplus(dt_t + bias_h) (or dt_t + bias_h),  alpha_t = exp(delta_t a_h)
+//   S_t = alpha_t S_{t-1} + delta_t x_t b_t^T,   y_t = S_t c_t + d_h x_t
+//
+// The rows of a state (one per value) never mix, so a warp walks the tokens with
+// its rows in registers: a thread holds 4 rows x 8 columns, DK/8 lanes a row.  A
+// token costs a lane 32 multiplies, 32 multiply-adds for the update and 32 for the
+// read-out, done on packed fp32 pairs, and a transposed reduction that leaves each
+// lane one row's sum (5 shuffles for 4 rows).  Tokens come in tiles of 32 by
+// cp.async, one tile ahead.
+//
+// The tokens of a segment follow one another, so one segment per sequence would
+// leave most SMs without work.  The sequence is cut into segments (find_seg): a
+// first pass forms each segment's own state from zero and its decay, combine_kernel
+// chains them, and the second pass runs every segment from its start state.
+#include "gdn_ssm_common.cuh"
+
+namespace gdn {
+namespace ssm {
+
+constexpr int kTile = 32;        // tokens per tile
+constexpr int kRows = 4;         // state rows per thread
+constexpr int kCols = 8;         // state columns per thread
+
+struct RowParams {
+    const void *x, *b, *c;
+    const float *dt, *a, *d, *dt_bias;
+    int64_t x_row, b_row, c_row;
+    int HK, HV, dv;
+    bool softplus;
+    void *y;
+    float *hT;               // null: not wanted
+    const float *h0;         // null: zero
+    float *seg_state;        // [segments][HV][dv][dk]: own states (first pass), start states (second)
+    float *seg_decay;        // [segments][HV]
+    bool chained;            // the slots hold every segment's start state (hT may then alias h0)
+    SegMap map;
+};
+
+__device__ __forceinline__ void cp16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src)
+                 : "memory");
+}
+
+// a thread's 8 columns: two float4 half a row apart (fp32: conflict-free 16-byte
+// reads) or 8 consecutive ones (bf16: one 16-byte read)
+template <int DK, typename T>
+__device__ __forceinline__ int col_of(int lane_in_row, int quad) {
+    return sizeof(T) == 4 ? quad * (DK / 2) + 4 * lane_in_row : 8 * lane_in_row + 4 * quad;
+}
+__device__ __forceinline__ void load_cols(const float *row, int l, int dk, float2 (&v)[4]) {
+    const float4 p = *reinterpret_cast<const float4 *>(row + 4 * l);
+    const float4 q = *reinterpret_cast<const float4 *>(row + dk / 2 + 4 * l);
+    v[0] = make_float2(p.x, p.y);
+    v[1] = make_float2(p.z, p.w);
+    v[2] = make_float2(q.x, q.y);
+    v[3] = make_float2(q.z, q.w);
+}
+__device__ __forceinline__ void load_cols(const __nv_bfloat16 *row, int l, int, float2 (&v)[4]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(row + 8 * l);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long ua, ub, ud;
+    memcpy(&ua, &a, 8);
+    memcpy(&ub, &b, 8);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(ud) : "l"(ua), "l"(ub));
+    float2 d;
+    memcpy(&d, &ud, 8);
+    return d;
+}
+
+template <int DK>
+__host__ __device__ constexpr int rows_per_warp() { return 32 / (DK / kCols) * kRows; }
+
+// one tile of raw tokens
+template <int DK, typename T>
+struct Tile {
+    T b[kTile][DK];
+    T c[kTile][DK];
+    T x[kTile][128];
+    float delta[kTile], alpha[kTile];
+};
+
+// READ: the second pass (start states, read-out, final state); otherwise the first
+template <int DK, typename T, bool READ>
+__global__ void __launch_bounds__(128)
+scan_rows_kernel(const RowParams p) {
+    constexpr int LPR = DK / kCols;          // lanes per row group
+    constexpr int RPW = rows_per_warp<DK>();
+    constexpr int V = 16 / (int)sizeof(T);   // elements per 16 bytes
+    extern __shared__ __align__(16) uint8_t raw[];
+    Tile<DK, T> *tiles = reinterpret_cast<Tile<DK, T> *>(raw);
+    const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rpc = (nt >> 5) * RPW;         // rows per CTA
+    const int bands = p.dv / rpc;
+    const int slot = blockIdx.x / (p.HV * bands), hb = blockIdx.x - slot * (p.HV * bands);
+    const Seg seg = find_seg(p.map, slot);
+    if (!seg.ok) return;
+    if (!READ && seg.last) return;           // nothing follows: its own state is not needed
+    const int h = hb / bands, row0 = (hb - h * bands) * rpc;
+    const int ck = h / (p.HV / p.HK);
+    const int l = lane % LPR, grp = lane / LPR;
+    const int lrow = warp * RPW + grp * kRows;        // first row of this thread in the CTA
+    const T *xp = static_cast<const T *>(p.x) + seg.t0 * p.x_row + (int64_t)h * p.dv + row0;
+    const T *bp = static_cast<const T *>(p.b) + seg.t0 * p.b_row + (int64_t)ck * DK;
+    const T *cp = static_cast<const T *>(p.c) + seg.t0 * p.c_row + (int64_t)ck * DK;
+    const float *dtp = p.dt + seg.t0 * p.HV + h;
+    const float ah = p.a[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    const float dh = READ && p.d ? p.d[h] : 0.f;
+    const size_t st = ((size_t)slot * p.HV + h) * p.dv * DK;      // this segment's slot
+    const size_t sq = ((size_t)seg.n * p.HV + h) * p.dv * DK;           // this sequence's state
+
+    float2 S[kRows][4];
+    const float *src = nullptr;
+    if (READ) src = p.chained ? p.seg_state + st : p.h0 ? p.h0 + sq : nullptr;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (src) f = *reinterpret_cast<const float4 *>(src + (size_t)(row0 + lrow + r) * DK + col_of<DK, T>(l, q));
+            S[r][2 * q] = make_float2(f.x, f.y);
+            S[r][2 * q + 1] = make_float2(f.z, f.w);
+        }
+
+    const int ntiles = (seg.len + kTile - 1) / kTile;
+    auto issue = [&](int k) {
+        if (k < ntiles) {
+            Tile<DK, T> &t = tiles[k & 1];
+            const int64_t at = (int64_t)k * kTile;
+            const int m = min(kTile, seg.len - k * kTile);
+            for (int i = tid; i < m * (DK / V); i += nt) {
+                const int r = i / (DK / V), e = (i - r * (DK / V)) * V;
+                cp16(&t.b[r][e], bp + (at + r) * p.b_row + e);
+                if (READ) cp16(&t.c[r][e], cp + (at + r) * p.c_row + e);
+            }
+            const int xv = rpc / V;
+            for (int i = tid; i < m * xv; i += nt) {
+                const int r = i / xv, e = (i - r * xv) * V;
+                cp16(&t.x[r][e], xp + (at + r) * p.x_row + e);
+            }
+            for (int i = tid; i < m; i += nt) {
+                const float dl = step_size(dtp[(at + i) * p.HV], bias, p.softplus);
+                t.delta[i] = dl;
+                t.alpha[i] = expf(dl * ah);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    issue(0);
+    float decay = 1.f;
+    for (int k = 0; k < ntiles; ++k) {
+        issue(k + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        const Tile<DK, T> &t = tiles[k & 1];
+        const int m = min(kTile, seg.len - k * kTile);
+        T *yo = READ ? static_cast<T *>(p.y) + ((seg.t0 + (int64_t)k * kTile) * p.HV + h) * p.dv + row0 : nullptr;
+        for (int i = 0; i < m; ++i) {
+            float2 bb[4];
+            load_cols(t.b[i], l, DK, bb);
+            const float al = t.alpha[i], dl = t.delta[i];
+            const float2 al2 = make_float2(al, al);
+            float xr[kRows], acc[kRows];
+            {
+                const float4 f = load4(&t.x[i][lrow]);
+                xr[0] = f.x;
+                xr[1] = f.y;
+                xr[2] = f.z;
+                xr[3] = f.w;
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float u = dl * xr[r];
+                const float2 u2 = make_float2(u, u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[r][j] = fma2(S[r][j], al2, mul2(u2, bb[j]));
+            }
+            if (READ) {
+                float2 cc[4];
+                load_cols(t.c[i], l, DK, cc);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    float2 s2 = mul2(S[r][0], cc[0]);
+#pragma unroll
+                    for (int j = 1; j < 4; ++j) s2 = fma2(S[r][j], cc[j], s2);
+                    acc[r] = s2.x + s2.y;
+                }
+                // 4 rows over LPR lanes: halve the rows twice, then plain butterflies
+                const bool up = (lane & (LPR / 2)) != 0;
+                float k0 = up ? acc[2] : acc[0], k1 = up ? acc[3] : acc[1];
+                k0 += __shfl_xor_sync(0xffffffffu, up ? acc[0] : acc[2], LPR / 2);
+                k1 += __shfl_xor_sync(0xffffffffu, up ? acc[1] : acc[3], LPR / 2);
+                const bool up2 = (lane & (LPR / 4)) != 0;
+                float v = up2 ? k1 : k0;
+                v += __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, LPR / 4);
+#pragma unroll
+                for (int off = LPR / 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                if ((lane & (LPR / 4 - 1)) == 0) {
+                    const int r = (up ? 2 : 0) + (up2 ? 1 : 0);
+                    const float xv = up ? (up2 ? xr[3] : xr[2]) : (up2 ? xr[1] : xr[0]);
+                    yo[(int64_t)i * p.HV * p.dv + lrow + r] = from_f32<T>(fmaf(dh, xv, v));
+                }
+            } else {
+                decay *= al;
+            }
+        }
+        __syncthreads();
+    }
+    float *dst = READ ? (seg.last && p.hT ? p.hT + sq : nullptr) : p.seg_state + st;
+    if (dst) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<float4 *>(dst + (size_t)(row0 + lrow + r) * DK + col_of<DK, T>(l, q)) =
+                    make_float4(S[r][2 * q].x, S[r][2 * q].y, S[r][2 * q + 1].x, S[r][2 * q + 1].y);
+    }
+    if (!READ && row0 == 0 && tid == 0) p.seg_decay[(size_t)slot * p.HV + h] = decay;
+}
+
+// Chains the segments of each sequence and head: slot i is read as segment i's own
+// state and overwritten with its start state; the state behind the last segment
+// goes to hT where `whole` (then the last segment's own state is there too).
+// One thread per 4 elements; a handful of dependent steps over L2-resident slots.
+__global__ void __launch_bounds__(256)
+combine_kernel(float *seg_state, const float *seg_decay, const float *h0, float *hT, int HV, int elems,
+               bool whole, const SegMap map) {
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (e >= elems) return;
+    const int n = blockIdx.x / HV, h = blockIdx.x - n * HV;
+    const int s0 = map.table ? map.first[n] : n * map.nseg;
+    const int s1 = map.table ? map.first[n + 1] : s0 + map.nseg;
+    const size_t sq = ((size_t)n * HV + h) * elems + e;
+    float4 S = h0 ? *reinterpret_cast<const float4 *>(h0 + sq) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int end = whole ? s1 : s1 - 1;
+    for (int s = s0; s < end; ++s) {
+        float4 *slot = reinterpret_cast<float4 *>(seg_state + ((size_t)s * HV + h) * elems + e);
+        const float4 own = *slot;
+        const float g = seg_decay[(size_t)s * HV + h];
+        *slot = S;
+        S = make_float4(fmaf(g, S.x, own.x), fmaf(g, S.y, own.y), fmaf(g, S.z, own.z), fmaf(g, S.w, own.w));
+    }
+    if (whole) {
+        if (hT) *reinterpret_cast<float4 *>(hT + sq) = S;
+    } else {
+        *reinterpret_cast<float4 *>(seg_state + ((size_t)end * HV + h) * elems + e) = S;
+    }
+}
+
+// Segment table of a packed batch: one block, a running sum over tiles of 1024 sequences.
+__global__ void __launch_bounds__(1024)
+plan_kernel(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first) {
+    __shared__ int part[32];
+    __shared__ int base;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) base = 0;
+    __syncthreads();
+    for (int n0 = 0; n0 < N; n0 += 1024) {
+        const int n = n0 + tid;
+        int t0 = 0, len = 0, cnt = 0;
+        if (n < N) {
+            t0 = cu[n];
+            len = cu[n + 1] - t0;
+            cnt = len > 0 ? (len - 1) / seg_len + 1 : 1;
+        }
+        int inc = cnt;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
+        }
+        if (lane == 31) part[warp] = inc;
+        __syncthreads();
+        if (warp == 0) {
+            int q = part[lane];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, q, off);
+                if (lane >= off) q += y;
+            }
+            part[lane] = q;
+        }
+        __syncthreads();
+        const int at = base + inc - cnt + (warp ? part[warp - 1] : 0);
+        if (n < N) {
+            first[n] = at;
+            for (int i = 0; i < cnt && at + i < bound; ++i)
+                table[at + i] = make_int4(n, t0 + i * seg_len, min(seg_len, len - i * seg_len), i);
+        }
+        __syncthreads();
+        if (tid == 1023) base = at + cnt;
+        __syncthreads();
+    }
+    if (tid == 0) first[N] = base;
+}
+
+// ---- host: how the call is cut ----
+struct Cut {
+    int seg_len, nseg;      // tokens per segment; segments per sequence (without cu_seqlens)
+    int bound;              // segments at most, over all sequences
+    size_t table, first, decay, state, total;   // byte offsets in the workspace
+};
+
+static int ctas_per_state(const SsmArgs &a) {
+    const int rpw = a.dk == 128 ? rows_per_warp<128>() : a.dk == 64 ? rows_per_warp<64>() : rows_per_warp<32>();
+    const int warps = min(4, max(1, a.dv / rpw));
+    return a.dv / (warps * rpw);
+}
+
+// Segments are worth their first pass (2/5 of the second's arithmetic) while the SMs
+// have fewer than about 3 CTAs of 4 warps each without them; below 256 tokens a
+// segment's start and end states weigh as much as its tokens.
+static Cut cut_rows(const SsmArgs &a) {
+    Cut c{};
+    const bool packed = a.cu_seqlens != nullptr;
+    const int64_t longest = a.T > 0 ? a.T : 1;
+    const int64_t base = (int64_t)a.HV * ctas_per_state(a) * (packed ? 1 : a.N);
+    int64_t nseg = base >= 444 ? 1 : (444 + base - 1) / base;
+    int64_t len = (longest + nseg - 1) / nseg;
+    len = (len + kTile - 1) / kTile * kTile;
+    if (len < 256) len = 256;
+    if (len > (1 << 30)) len = 1 << 30;
+    c.seg_len = (int)len;
+    c.nseg = (int)((longest + len - 1) / len);
+    const int64_t bound = packed ? a.T / len + a.N : (int64_t)a.N * c.nseg;
+    c.bound = bound * a.HV * ctas_per_state(a) > 0x7fffffff ? -1 : (int)bound;   // grid.x
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    size_t off = 256;
+    c.table = off;
+    if (packed) off += up((size_t)bound * sizeof(int4));
+    c.first = off;
+    if (packed) off += up((size_t)(a.N + 1) * sizeof(int));
+    c.decay = off;
+    c.state = off;
+    if (packed || c.nseg > 1) {
+        off += up((size_t)bound * a.HV * sizeof(float));
+        c.state = off;
+        off += (size_t)bound * a.HV * a.dv * a.dk * sizeof(float);
+    }
+    c.total = packed || c.nseg > 1 ? off : 0;
+    return c;
+}
+
+template <int DK, typename T>
+static cudaError_t launch_rows(const SsmArgs &a, cudaStream_t stream) {
+    const Cut cut = cut_rows(a);
+    if (cut.bound < 0) return cudaErrorInvalidValue;
+    cudaError_t err = cudaSuccess;
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    const bool packed = a.cu_seqlens != nullptr;
+    RowParams p{a.x, a.b, a.c, a.dt, a.a, a.d, a.dt_bias, a.x_row, a.b_row, a.c_row, a.HK, a.HV, a.dv,
+                a.softplus, a.y, a.hT, a.h0, nullptr, nullptr, false,
+                SegMap{nullptr, nullptr, a.N, cut.nseg, a.T, cut.seg_len}};
+    if (cut.total) {
+        // the status word of gdn_read_status: nothing waits on the device here
+        err = cudaMemsetAsync(ws, 0, sizeof(unsigned int), stream);
+        if (err != cudaSuccess) return err;
+        p.seg_decay = reinterpret_cast<float *>(ws + cut.decay);
+        p.seg_state = reinterpret_cast<float *>(ws + cut.state);
+    }
+    if (packed) {
+        p.map.table = reinterpret_cast<int4 *>(ws + cut.table);
+        p.map.first = reinterpret_cast<int *>(ws + cut.first);
+        plan_kernel<<<1, 1024, 0, stream>>>(a.cu_seqlens, a.N, cut.seg_len, cut.bound,
+                                            reinterpret_cast<int4 *>(ws + cut.table),
+                                            reinterpret_cast<int *>(ws + cut.first));
+    }
+    const int warps = min(4, max(1, a.dv / rows_per_warp<DK>()));
+    const dim3 block(32 * warps);
+    const int bands = a.dv / (warps * rows_per_warp<DK>());
+    constexpr size_t smem = 2 * sizeof(Tile<DK, T>);
+    const dim3 grid((unsigned)((int64_t)cut.bound * a.HV * bands));
+    const bool cuts = packed ? a.T > cut.seg_len : cut.nseg > 1;
+    if (cuts) {
+        p.chained = true;
+        err = cudaFuncSetAttribute(scan_rows_kernel<DK, T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err != cudaSuccess) return err;
+        scan_rows_kernel<DK, T, false><<<grid, block, smem, stream>>>(p);
+        const int elems = a.dv * DK;
+        const dim3 cg((unsigned)((int64_t)a.N * a.HV), (elems / 4 + 255) / 256);
+        combine_kernel<<<cg, 256, 0, stream>>>(p.seg_state, p.seg_decay, a.h0, nullptr, a.HV, elems, false, p.map);
+    }
+    err = cudaFuncSetAttribute(scan_rows_kernel<DK, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    scan_rows_kernel<DK, T, true><<<grid, block, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace ssm
+
+bool ssm_supported(int dk, int dv) {
+    return (dk == 32 || dk == 64 || dk == 128) && (dv == 32 || dv == 64 || dv == 128);
+}
+
+size_t ssm_workspace_bytes(const SsmArgs &a) { return ssm::cut_rows(a).total; }
+
+cudaError_t launch_ssm_prefill(const SsmArgs &a, cudaStream_t stream) {
+    using namespace ssm;
+    const bool h = a.dtype == GDN_BF16;
+    switch (a.dk) {
+        case 32: return h ? launch_rows<32, __nv_bfloat16>(a, stream) : launch_rows<32, float>(a, stream);
+        case 64: return h ? launch_rows<64, __nv_bfloat16>(a, stream) : launch_rows<64, float>(a, stream);
+        default: return h ? launch_rows<128, __nv_bfloat16>(a, stream) : launch_rows<128, float>(a, stream);
+    }
+}
+
+}  // namespace gdn

@@ -118,6 +118,21 @@ def load_library() -> ctypes.CDLL:
                                                     i32, i32, i32, i32, ctypes.c_float, i32, vp,
                                                     vp, vp, vp, vp, i32, vp, ctypes.c_uint, vp,
                                                     sz, vp]
+            f32, u32 = ctypes.c_float, ctypes.c_uint
+            lib.gdn_ssm_prefill.restype = i32
+            lib.gdn_ssm_prefill.argtypes = [vp] * 9 + [i32, i64, i32, i32, i32, i32, i64, i64, i64,
+                                                       u32, i32, vp, vp, vp, sz, vp]
+            lib.gdn_ssm_prefill_workspace_size.restype = sz
+            lib.gdn_ssm_prefill_workspace_size.argtypes = [i32, i64, i32, i32, i32, i32, i32, i32]
+            lib.gdn_ssm_step.restype = i32
+            lib.gdn_ssm_step.argtypes = [vp] * 9 + [i32, vp, vp, i32, i32, i32, i32, i32, i64, u32,
+                                                    i32, vp, vp]
+            lib.gdn_gated_norm.restype = i32
+            lib.gdn_gated_norm.argtypes = [vp, vp, vp, i64, i32, i32, i64, i64, i32, f32, u32, i32,
+                                           vp, vp]
+            lib.gdn_residual_norm.restype = i32
+            lib.gdn_residual_norm.argtypes = [vp] * 5 + [i64, i32, f32, f32, u32, i32, i32, vp, vp,
+                                                         vp]
             _handle = lib
     return _handle
 
