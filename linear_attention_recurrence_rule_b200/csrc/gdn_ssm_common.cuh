@@ -49,6 +49,15 @@ __device__ __forceinline__ Seg find_seg(const SegMap &m, int s) {
     return r;
 }
 
+// Segment table of a packed batch; the chaining of the segments (gdn_ssm_rows.cu).
+cudaError_t launch_plan(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first, cudaStream_t stream);
+cudaError_t launch_combine(float *seg_state, const float *seg_decay, const float *h0, float *hT, int N, int HV, int elems,
+                           bool whole, const SegMap &map, cudaStream_t stream);
+// the tensor-core scan (gdn_ssm_tc.cu)
+bool tc_supported(const SsmArgs &a);
+size_t tc_workspace_bytes(const SsmArgs &a);
+cudaError_t launch_tc(const SsmArgs &a, cudaStream_t stream);
+
 // log(1 + e^x), finite and accurate at both ends
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 

@@ -302,6 +302,17 @@ plan_kernel(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *
     if (tid == 0) first[N] = base;
 }
 
+cudaError_t launch_plan(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first, cudaStream_t stream) {
+    plan_kernel<<<1, 1024, 0, stream>>>(cu, N, seg_len, bound, table, first);
+    return cudaGetLastError();
+}
+cudaError_t launch_combine(float *seg_state, const float *seg_decay, const float *h0, float *hT, int N, int HV, int elems,
+                           bool whole, const SegMap &map, cudaStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)N * HV), (elems / 4 + 255) / 256);
+    combine_kernel<<<grid, 256, 0, stream>>>(seg_state, seg_decay, h0, hT, HV, elems, whole, map);
+    return cudaGetLastError();
+}
+
 // ---- host: how the call is cut ----
 struct Cut {
     int seg_len, nseg;      // tokens per segment; segments per sequence (without cu_seqlens)
@@ -369,9 +380,9 @@ static cudaError_t launch_rows(const SsmArgs &a, cudaStream_t stream) {
     if (packed) {
         p.map.table = reinterpret_cast<int4 *>(ws + cut.table);
         p.map.first = reinterpret_cast<int *>(ws + cut.first);
-        plan_kernel<<<1, 1024, 0, stream>>>(a.cu_seqlens, a.N, cut.seg_len, cut.bound,
-                                            reinterpret_cast<int4 *>(ws + cut.table),
-                                            reinterpret_cast<int *>(ws + cut.first));
+        err = launch_plan(a.cu_seqlens, a.N, cut.seg_len, cut.bound, reinterpret_cast<int4 *>(ws + cut.table),
+                          reinterpret_cast<int *>(ws + cut.first), stream);
+        if (err != cudaSuccess) return err;
     }
     const int warps = min(4, max(1, a.dv / rows_per_warp<DK>()));
     const dim3 block(32 * warps);
@@ -384,9 +395,8 @@ static cudaError_t launch_rows(const SsmArgs &a, cudaStream_t stream) {
         err = cudaFuncSetAttribute(scan_rows_kernel<DK, T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
         scan_rows_kernel<DK, T, false><<<grid, block, smem, stream>>>(p);
-        const int elems = a.dv * DK;
-        const dim3 cg((unsigned)((int64_t)a.N * a.HV), (elems / 4 + 255) / 256);
-        combine_kernel<<<cg, 256, 0, stream>>>(p.seg_state, p.seg_decay, a.h0, nullptr, a.HV, elems, false, p.map);
+        err = launch_combine(p.seg_state, p.seg_decay, a.h0, nullptr, a.N, a.HV, a.dv * DK, false, p.map, stream);
+        if (err != cudaSuccess) return err;
     }
     err = cudaFuncSetAttribute(scan_rows_kernel<DK, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
@@ -400,10 +410,13 @@ bool ssm_supported(int dk, int dv) {
     return (dk == 32 || dk == 64 || dk == 128) && (dv == 32 || dv == 64 || dv == 128);
 }
 
-size_t ssm_workspace_bytes(const SsmArgs &a) { return ssm::cut_rows(a).total; }
+size_t ssm_workspace_bytes(const SsmArgs &a) {
+    return ssm::tc_supported(a) ? ssm::tc_workspace_bytes(a) : ssm::cut_rows(a).total;
+}
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, cudaStream_t stream) {
     using namespace ssm;
+    if (tc_supported(a)) return launch_tc(a, stream);
     const bool h = a.dtype == GDN_BF16;
     switch (a.dk) {
         case 32: return h ? launch_rows<32, __nv_bfloat16>(a, stream) : launch_rows<32, float>(a, stream);

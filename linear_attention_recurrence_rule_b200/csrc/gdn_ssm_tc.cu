@@ -1,0 +1,1008 @@
+// Selective state space scan on tensor cores: bf16 x, b, c with dk = 128 and value
+// heads of 64 or 128, fp32 states and sums.
+//
+//   S_t = alpha_t S_{t-1} + delta_t x_t b_t^T,   y_t = S_t c_t + d x_t
+//
+// In chunks of 128 tokens, with G the chunk's running sum of log alpha:
+//   y_i = e^{G_i} S_0 c_i + sum_{j<=i} P_ij x_j + d x_i,  P_ij = (c_i.b_j) e^{G_i-G_j} delta_j
+//   S_1 = e^{G_L} S_0 + sum_j w_j x_j b_j^T,               w_j = e^{G_L-G_j} delta_j
+// Nothing but the state ties the chunks, and the states add: a sequence is cut into
+// segments, whose own states (from zero) are formed first, chained, and then every
+// segment runs from its start state.  Three kernels:
+//
+//  * states_kernel, one CTA per (segment, value tile): S = sum_j (w_j x_j) b_j^T over
+//    the whole segment with the decays to the segment's END in w_j (all <= delta_j, so
+//    nothing overflows and nothing is rescaled on the way) -- one product with the
+//    tokens as its inner dimension, chunk by chunk from the end.  w_j x_j is a full
+//    fp32 value, so it enters as three bf16 terms (2^-24): the states returned to the
+//    caller carry fp32 accuracy.
+//  * combine_kernel (gdn_ssm_rows.cu): chains the segments in place; hT.
+//  * scan_kernel, one CTA per (segment, value tile), chunk by chunk: C B^T, the masked
+//    and decayed P, C S^T, P X and the next state, all on tcgen05 with the state in
+//    tensor memory.  Its state only feeds the bf16 y: w_j x_j enters as bf16 hi + lo, S
+//    as one bf16 operand and P as one bf16 operand, each term of y rounded once.
+//
+// A value tile is 128 columns where it can be: one head of 128, or two heads of 64 of
+// one group, which share C B^T and the loads of b and c; else one head of 64.
+// The state is kept transposed, S^T [dk lanes][value columns].
+//
+// scan_kernel's warps: loader (TMA), MMA issuer, table (step sizes, running sums, the
+// factors below), four of 4 warps each -- mask (C B^T -> P in the same tensor memory
+// columns), state (S -> bf16 operand, S times e^{G_L}), weight (w x -> hi + lo pieces of
+// 16 tokens through a ring of 3) and output.  The mask takes e^{G_i-G_j} as the decays
+// behind j in its 32-token block times those from there to i, both <= 1: one
+// exponential per row and block; only the diagonal blocks take one per element.  All
+// sums of log decays run over the tokens between the two ends (block sums), none is a
+// difference of running sums: a token that forgets everything (a log decay of
+// thousands) would leave such differences few digits for the tokens behind it.
+//
+// Waits are bounded (about 2 s): a wait that gives up records GDN_ERR_TIMEOUT in the
+// workspace's first word and every role winds down.
+#include <cuda.h>
+
+#include "gdn_ssm_common.cuh"
+#include "gdn_tc_common.cuh"
+#include "tc_primitives.cuh"
+#include "tma_host.h"
+
+namespace gdn {
+namespace ssm {
+namespace {
+
+using namespace tc;
+using namespace tcc;
+
+constexpr int L = 128;      // tokens per chunk
+constexpr int DK = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct TcParams {
+    const float *dt, *a, *d, *dt_bias, *h0;
+    int HK, HV;
+    bool soft;
+    __nv_bfloat16 *y;
+    float *seg_state, *seg_decay;
+    unsigned int *status;
+    bool chained;       // scan: start states from the slots (otherwise h0)
+    bool whole;         // states: the last segment's state is wanted too
+    bool wide_store;    // y is 32-byte aligned
+    SegMap map;
+};
+
+constexpr long long kWaitCycles = 4000000000LL, kDrainCycles = 100000000LL;
+struct Waiter {
+    uint64_t *bars;
+    volatile int *abort_flag;
+    unsigned int *status;
+    // false once the CTA has given up (the same in every lane)
+    __device__ bool operator()(int b, uint32_t parity) const {
+        bool ok = mbar_try_wait(&bars[b], parity);
+        if (!__all_sync(0xffffffffu, ok)) {
+            const long long t0 = clock64();
+            for (;;) {
+                ok = mbar_try_wait(&bars[b], parity);
+                if (__all_sync(0xffffffffu, ok)) break;
+                const bool stop = *abort_flag != 0 || clock64() - t0 > kWaitCycles;
+                if (__any_sync(0xffffffffu, stop)) {
+                    *abort_flag = 1;
+                    atomicExch(status, (unsigned int)GDN_ERR_TIMEOUT);
+                    return false;
+                }
+            }
+        }
+        return true;
+    }
+    __device__ void drain(int b, uint32_t parity) const {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bars[b], parity))
+            if (clock64() - t0 > kDrainCycles) return;
+    }
+};
+
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// one arrival for the warp, after all its lanes
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive(bar);
+}
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+// hardware 2^x (relative error about 2^-22; -inf gives 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void tmem_ld32r(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 u;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr));
+    return u;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 mulp(float2 a, float2 b) {
+    unsigned long long ua, ub, ud;
+    memcpy(&ua, &a, 8);
+    memcpy(&ub, &b, 8);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(ud) : "l"(ua), "l"(ub));
+    float2 d;
+    memcpy(&d, &ud, 8);
+    return d;
+}
+__device__ __forceinline__ float2 subp(float2 a, float2 b) {
+    unsigned long long ua, ub, ud;
+    memcpy(&ua, &a, 8);
+    memcpy(&ub, &b, 8);
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(ud) : "l"(ua), "l"(ub));
+    float2 d;
+    memcpy(&d, &ud, 8);
+    return d;
+}
+// x -> bf16 pair word, and the exact remainder
+__device__ __forceinline__ uint32_t take_bf16(float2 &x) {
+    const uint32_t w = pack_bf16x2(x.x, x.y);
+    x = subp(x, unpack2(w));
+    return w;
+}
+
+// Step sizes and log2 decays of one head's 128 tokens: lane l has tokens 4l .. 4l+3
+// (dt loaded ahead); tokens from `len` on have step size 0.  A log2 decay below -150
+// is taken as -150: every factor with that token in it is 0 in fp32 either way, and
+// the sums of the tokens around it keep their digits.
+struct HeadTab {
+    float ah, bias;   // a * log2 e, dt_bias
+};
+__device__ __forceinline__ void steps4(const float (&dt)[4], const HeadTab &t, int lane, int len, bool soft,
+                                       float (&delta)[4], float (&g)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool in = 4 * lane + i < len;
+        delta[i] = in ? step_size(dt[i], t.bias, soft) : 0.f;
+        g[i] = in ? fmaxf(delta[i] * t.ah, -150.f) : 0.f;
+    }
+}
+__device__ __forceinline__ void load_dt4(const float *dt, int64_t t0, int HV, int h, int lane, int len, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 4 * lane + i;
+        v[i] = t < len ? __ldg(dt + (t0 + t) * HV + h) : 0.f;
+    }
+}
+// Sums of g inside the 32-token blocks (8 lanes): pre[i] up to and including a token,
+// suf[i] behind it; tot[q] the blocks' totals.  Sums over longer spans add whole blocks
+// to these, so no span's sum is a difference of larger ones.
+__device__ __forceinline__ void block_sums(const float (&g)[4], int lane, float (&pre)[4], float (&suf)[4],
+                                           float (&tot)[4]) {
+    const float own = (g[0] + g[1]) + (g[2] + g[3]);
+    float up = own, down = own;
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, up, off), d = __shfl_down_sync(0xffffffffu, down, off);
+        if ((lane & 7) >= off) up += u;
+        if ((lane & 7) + off < 8) down += d;
+    }
+    float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
+    if ((lane & 7) == 0) before = 0.f;
+    if ((lane & 7) == 7) after = 0.f;
+    pre[0] = before + g[0];
+    pre[1] = pre[0] + g[1];
+    pre[2] = pre[1] + g[2];
+    pre[3] = pre[2] + g[3];
+    suf[3] = after;
+    suf[2] = after + g[3];
+    suf[1] = suf[2] + g[2];
+    suf[0] = suf[1] + g[1];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tot[q] = __shfl_sync(0xffffffffu, down, 8 * q);
+}
+// the totals of the blocks behind the lane's own
+__device__ __forceinline__ float blocks_behind(const float (&tot)[4], int lane) {
+    const int q = lane >> 3;
+    return q == 3 ? 0.f : q == 2 ? tot[3] : q == 1 ? tot[2] + tot[3] : (tot[1] + tot[2]) + tot[3];
+}
+
+// -------------------------------------------------------------------- segments' own states
+template <int VT, int NH>
+struct StatesCfg {
+    static constexpr uint32_t XT = VT * 256;                 // x tile: 128 rows
+    static constexpr uint32_t STAGE = 32768 + XT;            // b tile, x tile
+    static constexpr uint32_t TERM = VT * 64;                // one bf16 term of 32 tokens
+    static constexpr int NS = 3;                             // pieces in the ring
+    static constexpr uint32_t O_W = 2 * STAGE;
+    static constexpr uint32_t O_TAB = O_W + NS * 3 * TERM;   // w [2][NH][128]
+    static constexpr uint32_t O_BAR = O_TAB + 2 * NH * 512;
+    static constexpr uint32_t BYTES = O_BAR + 256 + 1024;
+};
+static_assert(StatesCfg<128, 2>::BYTES <= 232448, "shared memory");
+constexpr int kStWorkers = 8, kStWork0 = 4, kStThreads = (kStWork0 + kStWorkers) * 32;
+enum StBar { SB_F0, SB_F1, SB_E0, SB_E1, SB_TF0, SB_TF1, SB_TE0, SB_TE1, SB_WF0, SB_WE0 = SB_WF0 + 3,
+             SB_DONE = SB_WE0 + 3, SB_COUNT };
+
+template <int VT, int NH>
+__global__ void __launch_bounds__(kStThreads, 1)
+states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b, const TcParams p) {
+    using Cfg = StatesCfg<VT, NH>;
+    constexpr int DV = VT / NH;
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::O_BAR);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cfg::O_BAR + 8 * SB_COUNT);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cfg::O_BAR + 8 * SB_COUNT + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = p.HV / NH;
+    const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
+    const Seg seg = find_seg(p.map, slot);
+    if (!seg.ok || (seg.last && !p.whole)) return;
+    const int nch = (seg.len + L - 1) / L;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[SB_F0 + i], 1);
+            mbar_init(&bars[SB_E0 + i], 1 + kStWorkers);
+            mbar_init(&bars[SB_TF0 + i], 1);
+            mbar_init(&bars[SB_TE0 + i], kStWorkers);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bars[SB_WF0 + i], kStWorkers);
+            mbar_init(&bars[SB_WE0 + i], 1);
+        }
+        mbar_init(&bars[SB_DONE], 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 3) tmem_alloc(tslot, 128);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const Waiter wt{bars, abort_flag, p.status};
+    auto chunk_of = [&](int j) { return nch - 1 - j; };    // from the end
+    auto len_of = [&](int j) { return min(L, seg.len - chunk_of(j) * L); };
+    bool ok = true;
+
+    if (warp == 0) {
+        int issued = 0;
+        for (int j = 0; j < nch; ++j) {
+            const int s = j & 1;
+            if (j >= 2) ok = wt(SB_E0 + s, (uint32_t)(((j >> 1) - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+                uint8_t *st = sm + s * Cfg::STAGE;
+                uint64_t *full = &bars[SB_F0 + s];
+                const int t = (int)(seg.t0 + (int64_t)chunk_of(j) * L);
+                const int gb = head / (p.HV / p.HK) * DK;
+                mbar_arrive_expect_tx(full, Cfg::STAGE);
+                tma_load_2d(st, &tm_b, full, gb, t);
+                tma_load_2d(st + 16384, &tm_b, full, gb + 64, t);
+#pragma unroll
+                for (int q = 0; q < VT / 64; ++q)
+                    tma_load_2d(st + 32768 + q * 16384, &tm_x, full, head * DV + 64 * q, t);
+            }
+            issued = j + 1;
+            __syncwarp();
+        }
+        // no load stays in flight behind this CTA, whatever the other roles do
+        for (int j = issued > 2 ? issued - 2 : 0; j < issued; ++j) wt.drain(SB_F0 + (j & 1), (uint32_t)((j >> 1) & 1));
+    } else if (warp == 1) {
+        const uint32_t id = idesc_bf16(128, VT, true, true);
+        for (int j = 0; j < nch && ok; ++j) {
+            const int s = j & 1;
+            ok = wt(SB_F0 + s, (uint32_t)((j >> 1) & 1));
+            const uint64_t a0 = sdesc_sw128(sb + s * Cfg::STAGE, 16384, 1024);
+            for (int q = 0; q < 4 && ok; ++q) {
+                const int pc = 4 * j + q, r = pc % 3;
+                ok = wt(SB_WF0 + r, (uint32_t)((pc / 3) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t b0 = sdesc_sw128(sb + Cfg::O_W + r * 3 * Cfg::TERM, 4096, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int t = 0; t < 3; ++t)
+                            mma_bf16(tmem, desc_add(a0, q * 4096 + k * 2048), desc_add(b0, t * Cfg::TERM + k * 2048),
+                                     id, pc > 0 || k > 0 || t > 0);
+                    mma_commit(&bars[SB_WE0 + r]);
+                    if (q == 3) mma_commit(&bars[SB_E0 + s]);
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) mma_commit(&bars[SB_DONE]);
+        __syncwarp();
+        wt.drain(SB_DONE, 0);
+    } else if (warp == 2) {
+        HeadTab ht[NH];
+        float run[NH], dt[NH][4];
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+            ht[e] = {p.a[head + e] * kLog2e, p.dt_bias ? p.dt_bias[head + e] : 0.f};
+            run[e] = 0.f;
+            if (nch > 0) load_dt4(p.dt, seg.t0 + (int64_t)chunk_of(0) * L, p.HV, head + e, lane, len_of(0), dt[e]);
+        }
+        for (int j = 0; j < nch && ok; ++j) {
+            const int s = j & 1;
+            if (j >= 2) ok = wt(SB_TE0 + s, (uint32_t)(((j >> 1) - 1) & 1));
+            if (!ok) break;
+#pragma unroll
+            for (int e = 0; e < NH; ++e) {
+                float delta[4], g[4], pre[4], suf[4], tot[4];
+                steps4(dt[e], ht[e], lane, len_of(j), p.soft, delta, g);
+                if (j + 1 < nch) load_dt4(p.dt, seg.t0 + (int64_t)chunk_of(j + 1) * L, p.HV, head + e, lane, L, dt[e]);
+                block_sums(g, lane, pre, suf, tot);
+                const float behind = blocks_behind(tot, lane) + run[e];
+                float4 w;
+                w.x = delta[0] * ex2(suf[0] + behind);
+                w.y = delta[1] * ex2(suf[1] + behind);
+                w.z = delta[2] * ex2(suf[2] + behind);
+                w.w = delta[3] * ex2(suf[3] + behind);
+                reinterpret_cast<float4 *>(sm + Cfg::O_TAB + (s * NH + e) * 512)[lane] = w;
+                run[e] += (tot[0] + tot[1]) + (tot[2] + tot[3]);
+            }
+            warp_arrive(&bars[SB_TF0 + s]);
+        }
+        if (lane < NH) {
+            float r = run[0];
+            if (NH == 2 && lane == 1) r = run[NH - 1];
+            p.seg_decay[(size_t)slot * p.HV + head + lane] = ex2(r);
+        }
+    } else if (warp >= kStWork0) {
+        const int tid = threadIdx.x - kStWork0 * 32, row = tid >> 3, pc8 = tid & 7;
+        for (int j = 0; j < nch && ok; ++j) {
+            const int s = j & 1, len = len_of(j);
+            ok = wt(SB_F0 + s, (uint32_t)((j >> 1) & 1)) && wt(SB_TF0 + s, (uint32_t)((j >> 1) & 1));
+            const uint32_t stage = sb + s * Cfg::STAGE;
+            const float *tab = reinterpret_cast<const float *>(sm + Cfg::O_TAB + s * NH * 512);
+            for (int q = 0; q < 4 && ok; ++q) {
+                const int pc = 4 * j + q, r = pc % 3;
+                if (pc >= 3) ok = wt(SB_WE0 + r, (uint32_t)((pc / 3 - 1) & 1));
+                if (!ok) break;
+                const int token = 32 * q + row;
+                const bool in = token < len;
+                const uint32_t dst0 = sb + Cfg::O_W + r * 3 * Cfg::TERM + row * 128 + pc8 * 16;
+#pragma unroll
+                for (int v = 0; v < VT / 64; ++v) {
+                    uint32_t hi[4] = {0, 0, 0, 0}, mid[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+                    if (in) {
+                        const uint4 u = lds128(stage + 32768 + v * 16384 + token * 128 + pc8 * 16);
+                        const float w = tab[(NH == 2 ? v : 0) * 128 + token];
+                        const float2 w2 = make_float2(w, w);
+                        const uint32_t xs[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float2 f = mulp(unpack2(xs[i]), w2);
+                            hi[i] = take_bf16(f);
+                            mid[i] = take_bf16(f);
+                            lo[i] = pack_bf16x2(f.x, f.y);
+                        }
+                    }
+                    const uint32_t dst = dst0 + v * 4096;
+                    sts128(dst, hi[0], hi[1], hi[2], hi[3]);
+                    sts128(dst + Cfg::TERM, mid[0], mid[1], mid[2], mid[3]);
+                    sts128(dst + 2 * Cfg::TERM, lo[0], lo[1], lo[2], lo[3]);
+                }
+                if (!in) {
+                    // another sequence's rows (or none): a NaN there must not meet the zeros
+                    sts128(stage + token * 128 + pc8 * 16, 0, 0, 0, 0);
+                    sts128(stage + 16384 + token * 128 + pc8 * 16, 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                warp_arrive(&bars[SB_WF0 + r]);
+            }
+            if (ok) {
+                warp_arrive(&bars[SB_E0 + s]);
+                warp_arrive(&bars[SB_TE0 + s]);
+            }
+        }
+        ok = ok && wt(SB_DONE, 0);
+        if (ok) {
+            tc_fence_after();
+            // lane quadrant warp % 4 (key indices), half of the columns
+            const int wq = warp - kStWork0, half = wq >> 2, k = 32 * (warp & 3) + lane;
+#pragma unroll
+            for (int g = 0; g < VT / 64; ++g) {
+                const int col = half * (VT / 2) + 32 * g;
+                float v[32];
+                if (nch > 0) {
+                    tmem_ld32r(tmem_addr(tmem, warp, col), v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                }
+                const int h = head + col / DV;
+                float *dst = p.seg_state + (((size_t)slot * p.HV + h) * DV + col % DV) * DK + k;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) dst[i * DK] = v[i];
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+    }
+}
+
+// -------------------------------------------------------------------- the scan
+template <int VT, int NH>
+struct ScanCfg {
+    static constexpr uint32_t XT = VT * 256;
+    static constexpr uint32_t PIECE = VT * 32;               // one bf16 term of 16 tokens
+    static constexpr int NS = 3;
+    static constexpr uint32_t O_C = 0, O_B = 32768, O_X = O_B + 65536;
+    static constexpr uint32_t O_S = O_X + 2 * XT;            // S as bf16: 128 rows (k) x VT
+    static constexpr uint32_t O_W = O_S + XT;
+    static constexpr uint32_t O_TAB = O_W + NS * 2 * PIECE;  // [2][NH] x [128]: running sum in the block, delta e^(decay
+                                                             // to its end), delta, w
+    static constexpr uint32_t O_BAR = O_TAB + 2 * NH * 2048;
+    static constexpr uint32_t BYTES = O_BAR + 512 + 1024;
+};
+static_assert(ScanCfg<128, 2>::BYTES <= 232448, "shared memory");
+constexpr int kScMask = 4, kScState = 8, kScWeight = 12, kScOut = 16, kScThreads = 20 * 32;
+enum ScBar { B_CF, B_CE, B_BF0, B_BF1, B_BE0, B_BE1, B_XF0, B_XF1, B_XE0, B_XE1, B_TF0, B_TF1, B_TE0, B_TE1,
+             B_CB, B_P, B_S, B_UD, B_WF0, B_WE0 = B_WF0 + 3, B_Y = B_WE0 + 3, B_YE, B_CL, B_DONE, B_COUNT };
+static_assert(8 * B_COUNT + 8 <= 384, "barriers");
+constexpr uint32_t T_CB = 0, T_Y1 = 128, T_Y2 = 256, T_S = 384;
+
+template <int VT, int NH>
+__global__ void __launch_bounds__(kScThreads, 1)
+scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
+            const __grid_constant__ CUtensorMap tm_c, const TcParams p) {
+    using Cfg = ScanCfg<VT, NH>;
+    constexpr int DV = VT / NH;
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::O_BAR);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cfg::O_BAR + 8 * B_COUNT);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cfg::O_BAR + 8 * B_COUNT + 4);
+    float *bt = reinterpret_cast<float *>(sm + Cfg::O_BAR + 384);   // block totals [2][NH][4]
+    float *gl = bt + 16;                                            // e^{G_L} [2][NH]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = p.HV / NH;
+    const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
+    const Seg seg = find_seg(p.map, slot);
+    if (!seg.ok || seg.len <= 0) return;
+    const int nch = (seg.len + L - 1) / L, last = nch - 1;
+    const int tail = seg.len - last * L;      // tokens of the last chunk
+    if (threadIdx.x == 0) {
+        mbar_init(&bars[B_CF], 1);
+        mbar_init(&bars[B_CE], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[B_BF0 + i], 1);
+            mbar_init(&bars[B_BE0 + i], 1);
+            mbar_init(&bars[B_XF0 + i], 1);
+            mbar_init(&bars[B_XE0 + i], 8);
+            mbar_init(&bars[B_TF0 + i], 1);
+            mbar_init(&bars[B_TE0 + i], 16);
+        }
+        mbar_init(&bars[B_CB], 1);
+        mbar_init(&bars[B_P], 4);
+        mbar_init(&bars[B_S], 4);
+        mbar_init(&bars[B_UD], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bars[B_WF0 + i], 4);
+            mbar_init(&bars[B_WE0 + i], 1);
+        }
+        mbar_init(&bars[B_Y], 1);
+        mbar_init(&bars[B_YE], 4);
+        mbar_init(&bars[B_CL], 4);
+        mbar_init(&bars[B_DONE], 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 3) tmem_alloc(tslot, 512);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const Waiter wt{bars, abort_flag, p.status};
+    auto par2 = [](int c) { return (uint32_t)((c >> 1) & 1); };          // phase of use c >> 1 (two buffers)
+    auto par2_before = [](int c) { return (uint32_t)(((c >> 1) - 1) & 1); };
+    auto table = [&](int c, int e) { return reinterpret_cast<float *>(sm + Cfg::O_TAB + ((c & 1) * NH + e) * 2048); };
+    bool ok = true;
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads
+        int nb = 0, nx = 0, nc = 0;
+        for (int c = 0; c < nch; ++c) {
+            const int s = c & 1, t = (int)(seg.t0 + (int64_t)c * L);
+            const int gb = head / (p.HV / p.HK) * DK;
+            if (c >= 2) ok = wt(B_BE0 + s, par2_before(c));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[B_BF0 + s], 32768);
+                tma_load_2d(sm + Cfg::O_B + s * 32768, &tm_b, &bars[B_BF0 + s], gb, t);
+                tma_load_2d(sm + Cfg::O_B + s * 32768 + 16384, &tm_b, &bars[B_BF0 + s], gb + 64, t);
+            }
+            nb = c + 1;
+            if (c >= 2) ok = wt(B_XE0 + s, par2_before(c));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[B_XF0 + s], Cfg::XT);
+#pragma unroll
+                for (int q = 0; q < VT / 64; ++q)
+                    tma_load_2d(sm + Cfg::O_X + s * Cfg::XT + q * 16384, &tm_x, &bars[B_XF0 + s], head * DV + 64 * q, t);
+            }
+            nx = c + 1;
+            if (c >= 1) ok = wt(B_CE, (uint32_t)((c - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[B_CF], 32768);
+                tma_load_2d(sm + Cfg::O_C, &tm_c, &bars[B_CF], gb, t);
+                tma_load_2d(sm + Cfg::O_C + 16384, &tm_c, &bars[B_CF], gb + 64, t);
+            }
+            nc = c + 1;
+            __syncwarp();
+        }
+        // no load stays in flight behind this CTA, whatever the other roles do
+        for (int c = nb > 2 ? nb - 2 : 0; c < nb; ++c) wt.drain(B_BF0 + (c & 1), par2(c));
+        for (int c = nx > 2 ? nx - 2 : 0; c < nx; ++c) wt.drain(B_XF0 + (c & 1), par2(c));
+        if (nc > 0) wt.drain(B_CF, (uint32_t)((nc - 1) & 1));
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMAs
+        const uint32_t id_cb = idesc_bf16(128, 128, false, false);
+        const uint32_t id_cs = idesc_bf16(128, VT, false, true);
+        const uint32_t id_px = idesc_bf16(128, DV, false, true);
+        const uint32_t id_up = idesc_bf16(128, VT, true, true);
+        const uint64_t cd = sdesc_sw128(sb + Cfg::O_C, 16, 1024);
+        const uint64_t sd = sdesc_sw128(sb + Cfg::O_S, 16384, 1024);
+        auto scores = [&](int c) {   // C B^T of chunk c
+            ok = ok && wt(B_CF, (uint32_t)(c & 1)) && wt(B_BF0 + (c & 1), par2(c));
+            if (c == last && tail < L) ok = ok && wt(B_CL, 0);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t bd = sdesc_sw128(sb + Cfg::O_B + (c & 1) * 32768, 16, 1024);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+                    mma_bf16(tmem + T_CB, desc_add(cd, off), desc_add(bd, off), id_cb, k > 0);
+                }
+                mma_commit(&bars[B_CB]);
+            }
+            __syncwarp();
+        };
+        scores(0);
+        for (int c = 0; c < nch && ok; ++c) {
+            const uint32_t btile = sb + Cfg::O_B + (c & 1) * 32768, xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
+            ok = wt(B_S, (uint32_t)(c & 1));
+            if (ok && c > 0) ok = wt(B_YE, (uint32_t)((c - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {       // C S^T
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_bf16(tmem + T_Y1, desc_add(cd, (k >> 2) * 16384 + (k & 3) * 32), desc_add(sd, k * 2048), id_cs, k > 0);
+                mma_commit(&bars[B_CE]);
+            }
+            __syncwarp();
+            if (c < last) {          // S^T += B^T (w x)
+                const uint64_t ad = sdesc_sw128(btile, 16384, 1024);
+                for (int q = 0; q < 8 && ok; ++q) {
+                    const int pc = 8 * c + q, r = pc % 3;
+                    ok = wt(B_WF0 + r, (uint32_t)((pc / 3) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t wd = sdesc_sw128(sb + Cfg::O_W + r * 2 * Cfg::PIECE, 2048, 1024);
+                    if (elect_one()) {
+                        mma_bf16(tmem + T_S, desc_add(ad, q * 2048), wd, id_up, 1);
+                        mma_bf16(tmem + T_S, desc_add(ad, q * 2048), desc_add(wd, Cfg::PIECE), id_up, 1);
+                        mma_commit(&bars[B_WE0 + r]);
+                        if (q == 7) mma_commit(&bars[B_UD]);
+                    }
+                    __syncwarp();
+                }
+            }
+            ok = ok && wt(B_P, (uint32_t)(c & 1)) && wt(B_XF0 + (c & 1), par2(c));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {       // P X
+#pragma unroll
+                for (int e = 0; e < NH; ++e) {
+                    const uint64_t xd = sdesc_sw128(xtile + e * 16384, 16384, 1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_bf16_ts(tmem + T_Y2 + DV * e, tmem + T_CB + 32 * (k >> 1) + 8 * (k & 1) + 16 * e,
+                                    desc_add(xd, k * 2048), id_px, k > 0);
+                }
+                mma_commit(&bars[B_Y]);
+                mma_commit(&bars[B_BE0 + (c & 1)]);
+            }
+            __syncwarp();
+            if (c < last) scores(c + 1);
+        }
+        if (elect_one()) mma_commit(&bars[B_DONE]);
+        __syncwarp();
+        wt.drain(B_DONE, 0);
+    } else if (warp == 2) {
+        // ------------------------------------------------ tables
+        HeadTab ht[NH];
+        float dt[NH][4];
+        auto len_of = [&](int c) { return c == last ? tail : L; };
+#pragma unroll
+        for (int e = 0; e < NH; ++e) {
+            ht[e] = {p.a[head + e] * kLog2e, p.dt_bias ? p.dt_bias[head + e] : 0.f};
+            load_dt4(p.dt, seg.t0, p.HV, head + e, lane, len_of(0), dt[e]);
+        }
+        for (int c = 0; c < nch && ok; ++c) {
+            if (c >= 2) ok = wt(B_TE0 + (c & 1), par2_before(c));
+            if (!ok) break;
+#pragma unroll
+            for (int e = 0; e < NH; ++e) {
+                float delta[4], g[4], pre[4], suf[4], tot[4];
+                steps4(dt[e], ht[e], lane, len_of(c), p.soft, delta, g);
+                if (c < last) load_dt4(p.dt, seg.t0 + (int64_t)(c + 1) * L, p.HV, head + e, lane, len_of(c + 1), dt[e]);
+                block_sums(g, lane, pre, suf, tot);
+                const float behind = blocks_behind(tot, lane);
+                float4 *t = reinterpret_cast<float4 *>(table(c, e));
+                t[lane] = make_float4(pre[0], pre[1], pre[2], pre[3]);
+                t[32 + lane] = make_float4(delta[0] * ex2(suf[0]), delta[1] * ex2(suf[1]), delta[2] * ex2(suf[2]),
+                                           delta[3] * ex2(suf[3]));
+                t[64 + lane] = make_float4(delta[0], delta[1], delta[2], delta[3]);
+                t[96 + lane] = make_float4(delta[0] * ex2(suf[0] + behind), delta[1] * ex2(suf[1] + behind),
+                                           delta[2] * ex2(suf[2] + behind), delta[3] * ex2(suf[3] + behind));
+                if (lane == 0) {
+                    gl[(c & 1) * NH + e] = ex2((tot[0] + tot[1]) + (tot[2] + tot[3]));
+                    *reinterpret_cast<float4 *>(bt + ((c & 1) * NH + e) * 4) = make_float4(tot[0], tot[1], tot[2], tot[3]);
+                }
+            }
+            warp_arrive(&bars[B_TF0 + (c & 1)]);
+        }
+    } else if (warp >= kScMask && warp < kScState) {
+        // ------------------------------------------------ mask: C B^T -> P (rows i = tokens)
+        const int w = warp - kScMask, i = 32 * w + lane;
+        for (int c = 0; c < nch && ok; ++c) {
+            ok = wt(B_TF0 + (c & 1), par2(c)) && wt(B_CB, (uint32_t)(c & 1));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t ta = tmem_addr(tmem, warp, T_CB + 32 * q);
+                uint32_t out[NH][16];
+                if (q <= w) {
+                    float v[32];
+                    tmem_ld32r(ta, v);
+#pragma unroll
+                    for (int e = 0; e < NH; ++e) {
+                        const float *t = table(c, e);
+                        const float pi = t[i];
+                        if (q < w) {
+                            // decays of the tokens behind block q, up to i
+                            const float *tot = bt + ((c & 1) * NH + e) * 4;
+                            float s = pi;
+#pragma unroll
+                            for (int m = 1; m < 3; ++m)
+                                if (m > q && m < w) s += tot[m];
+                            const float rf = ex2(s);
+                            const float2 rf2 = make_float2(rf, rf);
+                            const float4 *cf = reinterpret_cast<const float4 *>(t + 128 + 32 * q);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const float4 f = cf[u];
+                                const float2 p0 = mulp(mulp(make_float2(f.x, f.y), rf2), make_float2(v[4 * u], v[4 * u + 1]));
+                                const float2 p1 = mulp(mulp(make_float2(f.z, f.w), rf2), make_float2(v[4 * u + 2], v[4 * u + 3]));
+                                out[e][2 * u] = pack_bf16x2(p0.x, p0.y);
+                                out[e][2 * u + 1] = pack_bf16x2(p1.x, p1.y);
+                            }
+                        } else {
+                            const float4 *pj = reinterpret_cast<const float4 *>(t + 32 * q);
+                            const float4 *dj = reinterpret_cast<const float4 *>(t + 256 + 32 * q);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const float4 g4 = pj[u], d4 = dj[u];
+                                const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
+                                float f[4];
+#pragma unroll
+                                for (int b = 0; b < 4; ++b)
+                                    f[b] = 4 * u + b <= lane ? v[4 * u + b] * (ds[b] * ex2(pi - gs[b])) : 0.f;
+                                out[e][2 * u] = pack_bf16x2(f[0], f[1]);
+                                out[e][2 * u + 1] = pack_bf16x2(f[2], f[3]);
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NH; ++e)
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) out[e][u] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < NH; ++e) tmem_st16w(ta + 16 * e, out[e]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bars[B_P]);
+            warp_arrive(&bars[B_TE0 + (c & 1)]);
+        }
+    } else if (warp >= kScState && warp < kScWeight) {
+        // ------------------------------------------------ state (lanes k)
+        const int k = 32 * (warp - kScState) + lane;
+        const float *src = p.chained ? p.seg_state + ((size_t)slot * p.HV + head) * DV * DK
+                           : p.h0    ? p.h0 + ((size_t)seg.n * p.HV + head) * DV * DK
+                                     : nullptr;
+#pragma unroll 1
+        for (int col = 0; col < VT; col += 32) {
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = src ? __float_as_uint(src[(size_t)(col + i) * DK + k]) : 0u;
+            tmem_st32(tmem_addr(tmem, warp, T_S + col), v);
+        }
+        tmem_wait_st();
+        for (int c = 0; c < nch && ok; ++c) {
+            if (c > 0) ok = wt(B_UD, (uint32_t)((c - 1) & 1));
+            ok = ok && wt(B_TF0 + (c & 1), par2(c));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int g = 0; g < VT / 32; ++g) {
+                const uint32_t ta = tmem_addr(tmem, warp, T_S + 32 * g);
+                float v[32];
+                tmem_ld32r(ta, v);
+                const uint32_t dst = sb + Cfg::O_S + (g >> 1) * 16384;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    sts128(dst + sw128_chunk(k, 4 * (g & 1) + u), pack_bf16x2(v[8 * u], v[8 * u + 1]),
+                           pack_bf16x2(v[8 * u + 2], v[8 * u + 3]), pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
+                           pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+                if (c < last) {
+                    const float s = gl[(c & 1) * NH + (32 * g) / DV];
+                    uint32_t o[32];
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(v[u] * s);
+                    tmem_st32(ta, o);
+                }
+            }
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before();
+            warp_arrive(&bars[B_S]);
+            warp_arrive(&bars[B_TE0 + (c & 1)]);
+        }
+    } else if (warp >= kScWeight && warp < kScOut) {
+        // ------------------------------------------------ w x as hi + lo, 16 tokens a piece
+        const int tid = threadIdx.x - kScWeight * 32, row = tid >> 3, pc8 = tid & 7;
+        for (int c = 0; c < last && ok; ++c) {
+            ok = wt(B_XF0 + (c & 1), par2(c)) && wt(B_TF0 + (c & 1), par2(c));
+            const uint32_t xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
+            for (int q = 0; q < 8 && ok; ++q) {
+                const int pc = 8 * c + q, r = pc % 3;
+                if (pc >= 3) ok = wt(B_WE0 + r, (uint32_t)((pc / 3 - 1) & 1));
+                if (!ok) break;
+                const int token = 16 * q + row;
+#pragma unroll
+                for (int v = 0; v < VT / 64; ++v) {
+                    const uint4 u = lds128(xtile + v * 16384 + token * 128 + pc8 * 16);
+                    const float w = table(c, NH == 2 ? v : 0)[384 + token];
+                    const float2 w2 = make_float2(w, w);
+                    const uint32_t xs[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float2 f = mulp(unpack2(xs[i]), w2);
+                        hi[i] = take_bf16(f);
+                        lo[i] = pack_bf16x2(f.x, f.y);
+                    }
+                    const uint32_t dst = sb + Cfg::O_W + r * 2 * Cfg::PIECE + v * 2048 + row * 128 + pc8 * 16;
+                    sts128(dst, hi[0], hi[1], hi[2], hi[3]);
+                    sts128(dst + Cfg::PIECE, lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                warp_arrive(&bars[B_WF0 + r]);
+            }
+            if (ok) {
+                warp_arrive(&bars[B_XE0 + (c & 1)]);
+                warp_arrive(&bars[B_TE0 + (c & 1)]);
+            }
+        }
+        if (tail < L && ok) {
+            // rows behind the sequence are another's (or none): a NaN there must not
+            // meet P's zeros
+            ok = wt(B_XF0 + (last & 1), par2(last)) && wt(B_BF0 + (last & 1), par2(last));
+            if (ok) {
+                const uint32_t xtile = sb + Cfg::O_X + (last & 1) * Cfg::XT, btile = sb + Cfg::O_B + (last & 1) * 32768;
+                for (int r = tail + row; r < L; r += 16) {
+#pragma unroll
+                    for (int v = 0; v < VT / 64; ++v) sts128(xtile + v * 16384 + r * 128 + pc8 * 16, 0, 0, 0, 0);
+                    sts128(btile + r * 128 + pc8 * 16, 0, 0, 0, 0);
+                    sts128(btile + 16384 + r * 128 + pc8 * 16, 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                warp_arrive(&bars[B_CL]);
+            }
+        }
+    } else if (warp >= kScOut) {
+        // ------------------------------------------------ y (rows i = tokens)
+        const int i = 32 * (warp - kScOut) + lane;
+        float dh[NH];
+#pragma unroll
+        for (int e = 0; e < NH; ++e) dh[e] = p.d ? p.d[head + e] : 0.f;
+        for (int c = 0; c < nch && ok; ++c) {
+            ok = wt(B_TF0 + (c & 1), par2(c)) && wt(B_XF0 + (c & 1), par2(c)) && wt(B_Y, (uint32_t)(c & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const bool in = c < last || i < tail;
+            const uint32_t xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
+            __nv_bfloat16 *yr = p.y + ((seg.t0 + (int64_t)c * L + i) * p.HV + head) * DV;
+            float gam[NH];
+#pragma unroll
+            for (int e = 0; e < NH; ++e) {
+                const float *tot = bt + ((c & 1) * NH + e) * 4;
+                float s = table(c, e)[i];
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    if (m < warp - kScOut) s += tot[m];
+                gam[e] = ex2(s);
+            }
+#pragma unroll
+            for (int g = 0; g < VT / 16; ++g) {
+                float v1[16], v2[16];
+                tmem_ld16(tmem_addr(tmem, warp, T_Y1 + 16 * g), v1);
+                tmem_ld16(tmem_addr(tmem, warp, T_Y2 + 16 * g), v2);
+                const uint32_t xa = xtile + (g >> 2) * 16384;
+                const uint4 xu = lds128(xa + sw128_chunk(i, 2 * (g & 3))), xv = lds128(xa + sw128_chunk(i, 2 * (g & 3) + 1));
+                const uint32_t xw[8] = {xu.x, xu.y, xu.z, xu.w, xv.x, xv.y, xv.z, xv.w};
+                const float ga = gam[(16 * g) / DV], de = dh[(16 * g) / DV];
+                const float2 ga2 = make_float2(ga, ga), de2 = make_float2(de, de);
+                tmem_wait_ld();
+                uint32_t o[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    float2 s = fma2(ga2, make_float2(v1[2 * u], v1[2 * u + 1]), make_float2(v2[2 * u], v2[2 * u + 1]));
+                    s = fma2(de2, unpack2(xw[u]), s);
+                    o[u] = pack_bf16x2(s.x, s.y);
+                }
+                if (in) {
+                    if (p.wide_store) {
+                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(yr + 16 * g), "r"(o[0]),
+                                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                     : "memory");
+                    } else {
+                        reinterpret_cast<uint4 *>(yr + 16 * g)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        reinterpret_cast<uint4 *>(yr + 16 * g)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+            }
+            tc_fence_before();
+            warp_arrive(&bars[B_YE]);
+            warp_arrive(&bars[B_XE0 + (c & 1)]);
+            warp_arrive(&bars[B_TE0 + (c & 1)]);
+        }
+    }
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 148;
+    return n;
+}
+
+int heads_per_tile(const SsmArgs &a) { return a.dv == 64 && (a.HV / a.HK) % 2 == 0 ? 2 : 1; }
+
+struct TcCut {
+    int seg_len, nseg;
+    int64_t bound;
+    size_t table, first, decay, state, total;
+};
+
+// Segment length in chunks: the fewest waves of CTAs over the SMs times the chunks of
+// a wave, a segment counting 2 chunks more for its start and end states.
+TcCut cut_tc(const SsmArgs &a) {
+    TcCut c{};
+    const bool packed = a.cu_seqlens != nullptr;
+    const int64_t chunks = (a.T + L - 1) / L > 0 ? (a.T + L - 1) / L : 1, seqs = packed ? 1 : a.N;
+    const int64_t tiles = a.HV / heads_per_tile(a), sms = sm_count();
+    int64_t best = 0, best_cost = 0;
+    for (int64_t n = 1; n <= 64 && n <= chunks; ++n) {
+        const int64_t len = (chunks + n - 1) / n, segs = (chunks + len - 1) / len;
+        const int64_t waves = (segs * seqs * tiles + sms - 1) / sms;
+        const int64_t cost = waves * (len + 2);
+        if (best == 0 || cost < best_cost) {
+            best = len;
+            best_cost = cost;
+        }
+    }
+    c.seg_len = (int)(best * L);
+    c.nseg = (int)((chunks + best - 1) / best);
+    c.bound = packed ? a.T / c.seg_len + a.N : (int64_t)a.N * c.nseg;
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    size_t off = 256;
+    c.table = off;
+    if (packed) off += up((size_t)c.bound * sizeof(int4));
+    c.first = off;
+    if (packed) off += up((size_t)(a.N + 1) * sizeof(int));
+    c.decay = off;
+    off += up((size_t)c.bound * a.HV * sizeof(float));
+    c.state = off;
+    off += (size_t)c.bound * a.HV * a.dv * DK * sizeof(float);
+    c.total = off;
+    return c;
+}
+
+template <int VT, int NH>
+cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
+    const TcCut cut = cut_tc(a);
+    const int64_t grid = cut.bound * (a.HV / NH);
+    if (grid > 0x7fffffff || (int64_t)a.N * a.HV > 0x7fffffff) return cudaErrorInvalidValue;
+    const bool packed = a.cu_seqlens != nullptr;
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    cudaError_t err = cudaMemsetAsync(ws, 0, sizeof(unsigned int), stream);
+    if (err != cudaSuccess) return err;
+    const bool cuts = packed ? a.T > cut.seg_len : cut.nseg > 1;
+    const bool states = cuts || a.hT != nullptr;
+    TcParams p{a.dt, a.a, a.d, a.dt_bias, a.h0, a.HK, a.HV, a.softplus, static_cast<__nv_bfloat16 *>(a.y),
+               reinterpret_cast<float *>(ws + cut.state), reinterpret_cast<float *>(ws + cut.decay),
+               reinterpret_cast<unsigned int *>(ws), states, a.hT != nullptr,
+               (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0,
+               SegMap{nullptr, nullptr, a.N, cut.nseg, a.T, cut.seg_len}};
+    if (packed) {
+        p.map.table = reinterpret_cast<int4 *>(ws + cut.table);
+        p.map.first = reinterpret_cast<int *>(ws + cut.first);
+        err = launch_plan(a.cu_seqlens, a.N, cut.seg_len, (int)cut.bound, reinterpret_cast<int4 *>(ws + cut.table),
+                          reinterpret_cast<int *>(ws + cut.first), stream);
+        if (err != cudaSuccess) return err;
+    }
+    const uint64_t tokens = (uint64_t)(packed ? a.T : (int64_t)a.N * a.T);
+    CUtensorMap tx{}, tb{}, tcm{};
+    if (tokens > 0) {
+        const uint32_t box[2] = {64, (uint32_t)L};
+        const uint64_t dx[2] = {(uint64_t)a.HV * a.dv, tokens}, db[2] = {(uint64_t)a.HK * DK, tokens};
+        const uint64_t sx[1] = {(uint64_t)a.x_row * 2}, sbb[1] = {(uint64_t)a.b_row * 2}, sc[1] = {(uint64_t)a.c_row * 2};
+        if (!encode_bf16_map(&tx, a.x, 2, dx, sx, box) || !encode_bf16_map(&tb, a.b, 2, db, sbb, box) ||
+            !encode_bf16_map(&tcm, a.c, 2, db, sc, box))
+            return cudaErrorInvalidValue;
+    }
+    if (states) {
+        constexpr uint32_t bytes = StatesCfg<VT, NH>::BYTES;
+        err = cudaFuncSetAttribute(states_kernel<VT, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (err != cudaSuccess) return err;
+        states_kernel<VT, NH><<<(unsigned)grid, kStThreads, bytes, stream>>>(tx, tb, p);
+        err = launch_combine(p.seg_state, p.seg_decay, a.h0, a.hT, a.N, a.HV, a.dv * DK, p.whole, p.map, stream);
+        if (err != cudaSuccess) return err;
+    }
+    if (tokens > 0) {
+        constexpr uint32_t bytes = ScanCfg<VT, NH>::BYTES;
+        err = cudaFuncSetAttribute(scan_kernel<VT, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (err != cudaSuccess) return err;
+        scan_kernel<VT, NH><<<(unsigned)grid, kScThreads, bytes, stream>>>(tx, tb, tcm, p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tc_supported(const SsmArgs &a) { return a.dtype == GDN_BF16 && a.dk == DK && (a.dv == 64 || a.dv == 128); }
+size_t tc_workspace_bytes(const SsmArgs &a) { return cut_tc(a).total; }
+cudaError_t launch_tc(const SsmArgs &a, cudaStream_t stream) {
+    if (a.dv == 128) return launch_tiles<128, 1>(a, stream);
+    return heads_per_tile(a) == 2 ? launch_tiles<128, 2>(a, stream) : launch_tiles<64, 1>(a, stream);
+}
+
+}  // namespace ssm
+}  // namespace gdn
