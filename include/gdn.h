@@ -593,8 +593,11 @@ GDN_API size_t gdn_ssm_prefill_workspace_size(int N, int64_t T, int HK, int HV, 
  *   dt [N][HV] fp32; a, d, dt_bias as above; state, state_out [N][HV][dv][dk] fp32
  *   (the same buffer: in place; otherwise they must not overlap); y [N][HV][dv] dtype
  * flags: GDN_SSM_SOFTPLUS, GDN_CONV_SILU.  Supported: dk in {32, 64, 128},
- * 1 <= dv <= 256, widths as gdn_short_conv.  Alignment: states 16 bytes, the rest
- * their element's size.  N == 0: GDN_OK, nothing launched.
+ * 1 <= dv <= 256, widths as gdn_short_conv, N <= 262140.  Alignment: states and
+ * workspace 16 bytes, the rest their element's size.  workspace: device scratch of
+ * gdn_ssm_step_workspace_size(...) bytes (the convolved row in fp32), not to be shared
+ * by calls that may overlap.  Two launches, the second one dependent on the first.
+ * N == 0: GDN_OK, nothing launched.
  */
 GDN_API gdn_status gdn_ssm_step(const void *xbc, const float *dt, const float *a, const float *d,
                                 const float *dt_bias, const float *conv_weight,
@@ -602,7 +605,10 @@ GDN_API gdn_status gdn_ssm_step(const void *xbc, const float *dt, const float *a
                                 void *conv_state_out, int conv_width, const float *state,
                                 float *state_out, int N, int HK, int HV, int dk, int dv,
                                 int64_t xbc_row, unsigned flags, gdn_dtype dtype, void *y,
-                                gdn_stream_t stream);
+                                void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* Bytes of device workspace gdn_ssm_step needs (0 also for sizes it would reject). */
+GDN_API size_t gdn_ssm_step_workspace_size(int N, int HK, int HV, int dk, int dv);
 
 /*
  * ---- Norms around a block --------------------------------------------------

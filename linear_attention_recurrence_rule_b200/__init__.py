@@ -15,7 +15,8 @@ from .gdn import (GDN_BF16, GDN_F32, GDNError, gdn_chunk_prefill,  # noqa: F401
                   PROLOGUE_GATE_LOGITS, PROLOGUE_ALL, ROW_DECAY)
 from .ssm import (GATE_SILU, NORM_GATE_FIRST, NORM_UNIT_OFFSET, SSM_SOFTPLUS,  # noqa: F401
                   gdn_gated_norm, gdn_residual_norm, gdn_ssm_prefill,
-                  gdn_ssm_prefill_workspace_size, gdn_ssm_step)
+                  gdn_ssm_prefill_workspace_size, gdn_ssm_step,
+                  gdn_ssm_step_workspace_size)
 
 __all__ = ["gdn_chunk_prefill", "gdn_recurrent_step", "gdn_recurrent_verify", "gdn_recurrent_verify_workspace_size", "gdn_state_commit",
            "gdn_recurrent_commit_verify", "gdn_recurrent_commit_verify_workspace_size",
@@ -26,5 +27,6 @@ __all__ = ["gdn_chunk_prefill", "gdn_recurrent_step", "gdn_recurrent_verify", "g
            "PROLOGUE_ALL", "ROW_DECAY", "gdn_short_conv", "gdn_output_gate",
            "gdn_recurrent_step_layer", "gdn_chunk_prefill_layer",
            "gdn_chunk_prefill_layer_workspace_size", "CONV_SILU", "CONV_MAX_WIDTH",
-           "gdn_ssm_prefill", "gdn_ssm_prefill_workspace_size", "gdn_ssm_step", "gdn_gated_norm",
+           "gdn_ssm_prefill", "gdn_ssm_prefill_workspace_size", "gdn_ssm_step",
+           "gdn_ssm_step_workspace_size", "gdn_gated_norm",
            "gdn_residual_norm", "SSM_SOFTPLUS", "GATE_SILU", "NORM_GATE_FIRST", "NORM_UNIT_OFFSET"]

@@ -184,10 +184,12 @@ struct SsmStepArgs {
     int64_t xbc_row;
     gdn_dtype dtype;
     void *y;
+    void *workspace;
 };
 bool ssm_supported(int dk, int dv);
 size_t ssm_workspace_bytes(const SsmArgs &a);
 cudaError_t launch_ssm_prefill(const SsmArgs &a, cudaStream_t stream);
+size_t ssm_step_workspace_bytes(int N, int HK, int HV, int dk, int dv);
 cudaError_t launch_ssm_step(const SsmStepArgs &a, cudaStream_t stream);
 
 // ---- norms around a block (gdn_norm.cu) ----

@@ -23,9 +23,22 @@ gdn_status check_ssm_sizes(int N, int64_t T, int HK, int HV, int dk, int dv, gdn
     return GDN_OK;
 }
 
+gdn_status check_step_sizes(int N, int HK, int HV, int dk, int dv) {
+    if (N < 0 || HK <= 0 || HV <= 0 || dk <= 0 || dv <= 0 || HV % HK) return GDN_ERR_INVALID_ARG;
+    if (!gdn::decode_supported(dk, dv)) return GDN_ERR_UNSUPPORTED;
+    // the row in 32 bits; sequences in groups of four over grid.y
+    if ((int64_t)N * HV > kGrid || (int64_t)HV * dv + 2 * (int64_t)HK * dk > kGrid || N > 4 * 65535)
+        return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t gdn_ssm_step_workspace_size(int N, int HK, int HV, int dk, int dv) {
+    return check_step_sizes(N, HK, HV, dk, dv) == GDN_OK ? gdn::ssm_step_workspace_bytes(N, HK, HV, dk, dv) : 0;
+}
 
 size_t gdn_ssm_prefill_workspace_size(int N, int64_t T, int HK, int HV, int dk, int dv, gdn_dtype dtype,
                                       int varlen) {
@@ -80,13 +93,13 @@ gdn_status gdn_ssm_step(const void *xbc, const float *dt, const float *a, const 
                         const float *dt_bias, const float *conv_weight, const float *conv_bias,
                         const void *conv_state, void *conv_state_out, int conv_width,
                         const float *state, float *state_out, int N, int HK, int HV, int dk, int dv,
-                        int64_t xbc_row, unsigned flags, gdn_dtype dtype, void *y, gdn_stream_t stream) {
+                        int64_t xbc_row, unsigned flags, gdn_dtype dtype, void *y, void *workspace,
+                        size_t workspace_bytes, gdn_stream_t stream) {
     if (flags & ~(GDN_SSM_SOFTPLUS | GDN_CONV_SILU)) return GDN_ERR_INVALID_ARG;
-    if (N < 0 || HK <= 0 || HV <= 0 || dk <= 0 || dv <= 0 || HV % HK) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = check_step_sizes(N, HK, HV, dk, dv);
+    if (st != GDN_OK) return st;
     if (!known(dtype)) return GDN_ERR_INVALID_ARG;
-    if (!gdn::decode_supported(dk, dv)) return GDN_ERR_UNSUPPORTED;
     const int64_t C = (int64_t)HV * dv + 2 * (int64_t)HK * dk;
-    if ((int64_t)N * HV > kGrid || C > kGrid) return GDN_ERR_UNSUPPORTED;
     if (conv_weight && (conv_width < 2 || conv_width > GDN_CONV_MAX_WIDTH)) return GDN_ERR_UNSUPPORTED;
     if (N == 0) return GDN_OK;   // empty batch: buffers may be NULL
     if (!xbc || !dt || !a || !state || !state_out || !y) return GDN_ERR_INVALID_ARG;
@@ -99,9 +112,11 @@ gdn_status gdn_ssm_step(const void *xbc, const float *dt, const float *a, const 
         !aligned(dt, 4) || !aligned(a, 4) || !aligned(d, 4) || !aligned(dt_bias, 4) ||
         !aligned(conv_weight, 4) || !aligned(conv_bias, 4))
         return GDN_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < gdn::ssm_step_workspace_bytes(N, HK, HV, dk, dv)) return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return GDN_ERR_ALIGNMENT;
     gdn::SsmStepArgs s{xbc, dt, a, d, dt_bias, conv_weight, conv_bias, conv_state, conv_state_out,
                        conv_width, (flags & GDN_CONV_SILU) != 0, (flags & GDN_SSM_SOFTPLUS) != 0, state,
-                       state_out, N, HK, HV, dk, dv, xbc_row, dtype, y};
+                       state_out, N, HK, HV, dk, dv, xbc_row, dtype, y, workspace};
     const cudaError_t err = gdn::launch_ssm_step(s, reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -4,17 +4,16 @@
 //   u_t[ch] = act(bias[ch] + sum_{j<W} w[ch][j] in_{t-(W-1)+j}[ch])     (x | b | c)
 //   S <- alpha S + delta x b^T,   y = S c + d x       (delta, alpha as in gdn_ssm_rows.cu)
 //
-// Bound by the states' pass through memory: each fp32 element is loaded once
-// (128-bit, streaming) and stored once.  CTAs of 8 warps own a band of rows of one
-// (sequence, head) state, a row in DK/4 lanes; every lane has NB loads in flight
-// before anything else, and the convolution's loads (its 2 DK + band channels, W
-// taps) go out behind them, so that they cost no time of their own.  Each CTA of a
-// group convolves the group's b and c itself: W taps of 2 DK channels from L2 are
-// far less than its 32 KB of state.
-//
-// The carried inputs of the x channels belong to one CTA and move in place.  Those
-// of b and c are read by every CTA of the group: where they move in place, a small
-// second kernel does it; otherwise the group's first CTA writes them.
+// Two kernels:
+//  * step_row_kernel: a thread per channel (four sequences each, its taps loaded
+//    once) convolves the row into the workspace in fp32 and moves the carried inputs
+//    on -- nobody else reads a channel's inputs, so in place is as good as not; it
+//    also forms delta and alpha of every head.
+//  * ssm_step_kernel: bound by the states' pass through memory.  Each fp32 element is
+//    loaded once (128-bit, streaming) and stored once; a row lies in DK/4 lanes, and a
+//    lane issues its NB row loads before anything else.  It is launched as a dependent
+//    of the first kernel and loads states while that one still runs: the states do not
+//    depend on it.  The rows' sums are reduced transposed (9 shuffles for 8 rows).
 #include "gdn_ssm_common.cuh"
 
 namespace gdn {
@@ -23,151 +22,196 @@ namespace {
 using ssm::step_size;
 
 constexpr int kWarps = 8;
-constexpr int kMaxBand = 128;
+constexpr int kRowSeqs = 4;      // sequences per thread of step_row_kernel
 
-template <typename T>
-struct StepParams {
-    const T *xbc;
-    const float *dt, *a, *d, *dt_bias, *cw, *cb;
-    const T *cs;
-    T *cs_out;
-    const float *state;
-    float *state_out;
-    T *y;
-    int HK, HV, dv, W;       // W 0: no convolution
-    int64_t row;
-    bool conv_silu, soft;
-    bool move_bc;            // the carried inputs of b and c are written here (not in place)
+struct RowCall {
+    const float *dt, *a, *dt_bias, *cw, *cb;
+    float *row;              // [N][C]
+    float2 *gates;           // [N][HV] delta, alpha
+    int64_t xbc_row;
+    int N, C, HV;
+    bool silu, soft;
 };
 
-// the convolution of one channel for the sequence's new token; `move`: its carried
-// inputs go on by one token
-template <typename T>
-__device__ __forceinline__ float conv_channel(const StepParams<T> &p, int n, size_t C, int ch, bool move) {
-    const T in = p.xbc[(int64_t)n * p.row + ch];
-    const float vin = to_f32(in);
-    if (p.W == 0) return vin;
-    constexpr int MW = kConvMaxWidth;
-    const int W = p.W;
-    const T *cs = p.cs + (size_t)n * (W - 1) * C + ch;
-    const float *wr = p.cw + (size_t)ch * W;
-    T hist[MW - 1];
-    float wt[MW];
-#pragma unroll
-    for (int m = 0; m < MW - 1; ++m)
-        if (m < W - 1) hist[m] = cs[m * C];
-#pragma unroll
-    for (int m = 0; m < MW; ++m)
-        if (m < W) wt[m] = wr[m];
-    float acc = p.cb ? p.cb[ch] : 0.f;
-#pragma unroll
-    for (int m = 0; m < MW - 1; ++m)
-        if (m < W - 1) acc = fmaf(wt[m], to_f32(hist[m]), acc);
-#pragma unroll
-    for (int m = 0; m < MW; ++m)
-        if (m == W - 1) acc = fmaf(wt[m], vin, acc);
-    if (move) {
-        T *co = p.cs_out + (size_t)n * (W - 1) * C + ch;
-#pragma unroll
-        for (int m = 0; m < MW - 2; ++m)
-            if (m < W - 2) co[m * C] = hist[m + 1];
-        co[(W - 2) * C] = in;
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// W 0: no convolution.  grid.x: blocks of 256 channels, then the heads' gates
+template <typename T, int W>
+__global__ void __launch_bounds__(256)
+step_row_kernel(const T *__restrict__ xbc, const T *cs, T *cs_out, const RowCall p) {
+    let_dependents_start();
+    const int cblocks = (p.C + 255) / 256;
+    const int n0 = blockIdx.y * kRowSeqs;
+    if ((int)blockIdx.x >= cblocks) {
+        const int h = ((int)blockIdx.x - cblocks) * 256 + threadIdx.x;
+        if (h >= p.HV) return;
+        const float ah = p.a[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+        for (int n = n0; n < min(n0 + kRowSeqs, p.N); ++n) {
+            const float dl = step_size(p.dt[(size_t)n * p.HV + h], bias, p.soft);
+            p.gates[(size_t)n * p.HV + h] = make_float2(dl, expf(dl * ah));
+        }
+        return;
     }
-    // full-precision sigmoid: the convolved value goes into the fp32 state
-    return p.conv_silu ? acc / (1.f + expf(-acc)) : acc;
+    const int ch = blockIdx.x * 256 + threadIdx.x;
+    if (ch >= p.C) return;
+    constexpr int H = W > 1 ? W - 1 : 1;
+    T hist[kRowSeqs][H], in[kRowSeqs];
+    float wt[W > 0 ? W : 1];
+#pragma unroll
+    for (int i = 0; i < kRowSeqs; ++i) {
+        const int n = n0 + i;
+        if (n < p.N) {
+            in[i] = xbc[(int64_t)n * p.xbc_row + ch];
+            if (W > 0)
+#pragma unroll
+                for (int m = 0; m < W - 1; ++m) hist[i][m] = cs[((size_t)n * (W - 1) + m) * p.C + ch];
+        }
+    }
+    if (W > 0)
+#pragma unroll
+        for (int m = 0; m < W; ++m) wt[m] = p.cw[(size_t)ch * W + m];
+    const float bias = W > 0 && p.cb ? p.cb[ch] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kRowSeqs; ++i) {
+        const int n = n0 + i;
+        if (n >= p.N) break;
+        float v = to_f32(in[i]);
+        if (W > 0) {
+            float acc = bias;
+#pragma unroll
+            for (int m = 0; m < W - 1; ++m) acc = fmaf(wt[m], to_f32(hist[i][m]), acc);
+            acc = fmaf(wt[W > 0 ? W - 1 : 0], v, acc);
+#pragma unroll
+            for (int m = 0; m < W - 1; ++m)
+                cs_out[((size_t)n * (W - 1) + m) * p.C + ch] = m + 1 < W - 1 ? hist[i][m + 1 < H ? m + 1 : 0] : in[i];
+            // full-precision sigmoid: the convolved value goes into the fp32 state
+            v = p.silu ? acc / (1.f + expf(-acc)) : acc;
+        }
+        p.row[(size_t)n * p.C + ch] = v;
+    }
 }
 
-template <int DK, int NB, typename T>
-__global__ void __launch_bounds__(kWarps * 32, NB >= 8 ? 3 : 4)
-ssm_step_kernel(const StepParams<T> p) {
+// v[8] summed over the lanes of a row (LPR lanes): halves the values three times, then
+// plain butterflies; the lane with (its bits LPR/2, LPR/4, LPR/8) = j has row j's sum
+template <int LPR>
+__device__ __forceinline__ float reduce8(const float (&v)[8], int lane, int &j) {
+    float a[4], b[2];
+    const bool u0 = lane & (LPR / 2), u1 = lane & (LPR / 4), u2 = lane & (LPR / 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = (u0 ? v[4 + i] : v[i]) + __shfl_xor_sync(0xffffffffu, u0 ? v[i] : v[4 + i], LPR / 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) b[i] = (u1 ? a[2 + i] : a[i]) + __shfl_xor_sync(0xffffffffu, u1 ? a[i] : a[2 + i], LPR / 4);
+    float c = (u2 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, u2 ? b[0] : b[1], LPR / 8);
+#pragma unroll
+    for (int o = LPR / 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    j = (u0 ? 4 : 0) + (u1 ? 2 : 0) + (u2 ? 1 : 0);
+    return c;
+}
+
+struct StepCall {
+    const float *row;
+    const float2 *gates;
+    const float *d, *state;
+    float *state_out;
+    int HK, HV, dv;
+    size_t C;
+};
+
+template <int DK, typename T>
+__global__ void __launch_bounds__(kWarps * 32, 4)
+ssm_step_kernel(const StepCall p, T *__restrict__ y) {
+    constexpr int NB = 8;
     constexpr int LPR = DK / 4;             // lanes per state row
     constexpr int RPI = 32 / LPR;           // rows per warp instruction
-    constexpr int BAND = kWarps * RPI * NB;
-    __shared__ float sb[DK], sc[DK], sx[BAND];
     const int nh = blockIdx.x;
-    const int n = nh / p.HV, h = nh - n * p.HV;
-    const int R = p.HV / p.HK, g = h / R;
+    const int n = nh / p.HV, h = nh - n * p.HV, g = h / (p.HV / p.HK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = lane / LPR, col = (lane % LPR) * 4;
-    const int base = blockIdx.y * BAND;
-    const size_t off = (size_t)nh * p.dv * DK;
+    const int col = (lane % LPR) * 4;
+    // this warp's NB x RPI consecutive rows
+    const int row0 = (blockIdx.y * kWarps + warp) * NB * RPI + lane / LPR * NB;
+    const size_t off = (size_t)nh * p.dv * DK + col;
     const float *S = p.state + off;
     float *So = p.state_out + off;
-
     float4 s[NB];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const int row = base + (j * kWarps + warp) * RPI + sub;
-        s[j] = row < p.dv ? __ldcs(reinterpret_cast<const float4 *>(S + (size_t)row * DK + col))
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < NB; ++j)
+        s[j] = row0 + j < p.dv ? __ldcs(reinterpret_cast<const float4 *>(S + (size_t)(row0 + j) * DK))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    wait_for_previous();
+    const float *r = p.row + (size_t)n * p.C;
+    const float *bc = r + (size_t)p.HV * p.dv + (size_t)g * DK + col;
+    // (rows of the packed x | b | c may start anywhere: single loads)
+    float b[4], c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        b[i] = __ldcg(bc + i);
+        c[i] = __ldcg(bc + (size_t)p.HK * DK + i);
     }
-    const float delta = step_size(p.dt[nh], p.dt_bias ? p.dt_bias[h] : 0.f, p.soft);
-    const float alpha = expf(delta * p.a[h]);
+    const float2 gate = __ldcg(p.gates + nh);
     const float dh = p.d ? p.d[h] : 0.f;
-    const size_t C = (size_t)p.HV * p.dv + 2 * (size_t)p.HK * DK;
-    const int rows = min(BAND, p.dv - base);
-    const bool move_bc = p.move_bc && h == g * R && blockIdx.y == 0;
-    for (int i = threadIdx.x; i < 2 * DK + rows; i += kWarps * 32) {
-        if (i < 2 * DK) {
-            const bool isc = i >= DK;
-            const int ch = p.HV * p.dv + (isc ? p.HK * DK : 0) + g * DK + (isc ? i - DK : i);
-            (isc ? sc[i - DK] : sb[i]) = conv_channel(p, n, C, ch, move_bc);
-        } else {
-            const int r = i - 2 * DK;
-            sx[r] = conv_channel(p, n, C, h * p.dv + base + r, p.W > 0);
-        }
-    }
-    __syncthreads();
-    const float4 b = *reinterpret_cast<const float4 *>(sb + col);
-    const float4 c = *reinterpret_cast<const float4 *>(sc + col);
+    float x[NB], v[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) x[j] = row0 + j < p.dv ? __ldcg(r + (size_t)h * p.dv + row0 + j) : 0.f;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        const int r = (j * kWarps + warp) * RPI + sub, row = base + r;
-        const float x = row < p.dv ? sx[r] : 0.f;
-        const float u = delta * x;
+        const float u = gate.x * x[j];
         float4 ns;
-        ns.x = fmaf(alpha, s[j].x, u * b.x);
-        ns.y = fmaf(alpha, s[j].y, u * b.y);
-        ns.z = fmaf(alpha, s[j].z, u * b.z);
-        ns.w = fmaf(alpha, s[j].w, u * b.w);
-        float v = dot4(ns, c);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (row < p.dv) {
-            __stcs(reinterpret_cast<float4 *>(So + (size_t)row * DK + col), ns);
-            if (lane % LPR == 0) p.y[(size_t)nh * p.dv + row] = from_f32<T>(fmaf(dh, x, v));
-        }
+        ns.x = fmaf(gate.y, s[j].x, u * b[0]);
+        ns.y = fmaf(gate.y, s[j].y, u * b[1]);
+        ns.z = fmaf(gate.y, s[j].z, u * b[2]);
+        ns.w = fmaf(gate.y, s[j].w, u * b[3]);
+        if (row0 + j < p.dv) __stcs(reinterpret_cast<float4 *>(So + (size_t)(row0 + j) * DK), ns);
+        v[j] = ns.x * c[0] + ns.y * c[1] + ns.z * c[2] + ns.w * c[3];
     }
+    int j;
+    const float sum = reduce8<LPR>(v, lane, j);
+    float xj = x[0];
+#pragma unroll
+    for (int i = 1; i < NB; ++i) xj = j == i ? x[i] : xj;
+    if ((lane & (LPR / 8 - 1)) == 0 && row0 + j < p.dv)
+        y[(size_t)nh * p.dv + row0 + j] = from_f32<T>(fmaf(dh, xj, sum));
 }
 
-// carried inputs of the b and c channels, in place: out of the step kernel's way
-template <typename T>
-__global__ void __launch_bounds__(256)
-move_bc_kernel(const T *xbc, T *cs, int64_t row, size_t C, int first, int W) {
-    const int ch = first + blockIdx.y * 256 + threadIdx.x, n = blockIdx.x;
-    if (ch >= (int)C) return;
-    T *p = cs + (size_t)n * (W - 1) * C + ch;
-    for (int m = 0; m < W - 2; ++m) p[m * C] = p[(m + 1) * C];
-    p[(size_t)(W - 2) * C] = xbc[(int64_t)n * row + ch];
+template <typename T, int W>
+void launch_row(const SsmStepArgs &a, const RowCall &r, cudaStream_t stream) {
+    const dim3 grid((unsigned)((r.C + 255) / 256 + (r.HV + 255) / 256), (unsigned)((a.N + kRowSeqs - 1) / kRowSeqs));
+    step_row_kernel<T, W><<<grid, 256, 0, stream>>>(static_cast<const T *>(a.xbc), static_cast<const T *>(a.conv_state),
+                                                    static_cast<T *>(a.conv_state_out), r);
 }
 
 template <int DK, typename T>
 cudaError_t launch_dk(const SsmStepArgs &a, cudaStream_t stream) {
-    const bool conv = a.conv_w != nullptr;
-    const bool in_place = conv && a.conv_state == a.conv_state_out;
-    StepParams<T> p{static_cast<const T *>(a.xbc), a.dt, a.a, a.d, a.dt_bias, a.conv_w, a.conv_b,
-                    static_cast<const T *>(a.conv_state), static_cast<T *>(a.conv_state_out), a.state,
-                    a.state_out, static_cast<T *>(a.y), a.HK, a.HV, a.dv, conv ? a.conv_width : 0,
-                    a.xbc_row, a.conv_silu, a.softplus, conv && !in_place};
-    constexpr int NB = 8, BAND = kWarps * (32 / (DK / 4)) * NB;
-    const dim3 grid((unsigned)(a.N * a.HV), (unsigned)((a.dv + BAND - 1) / BAND));
-    ssm_step_kernel<DK, NB, T><<<grid, kWarps * 32, 0, stream>>>(p);
-    if (in_place) {
-        const int first = a.HV * a.dv, bc = 2 * a.HK * DK;
-        move_bc_kernel<T><<<dim3((unsigned)a.N, (unsigned)((bc + 255) / 256)), 256, 0, stream>>>(
-            p.xbc, p.cs_out, a.xbc_row, (size_t)first + bc, first, a.conv_width);
+    const int C = a.HV * a.dv + 2 * a.HK * DK;
+    float2 *gates = static_cast<float2 *>(a.workspace);
+    float *row = reinterpret_cast<float *>(gates + (size_t)a.N * a.HV);
+    const RowCall r{a.dt, a.a, a.dt_bias, a.conv_w, a.conv_b, row, gates, a.xbc_row, a.N, C, a.HV,
+                    a.conv_silu, a.softplus};
+    switch (a.conv_w ? a.conv_width : 0) {
+        case 0: launch_row<T, 0>(a, r, stream); break;
+        case 2: launch_row<T, 2>(a, r, stream); break;
+        case 3: launch_row<T, 3>(a, r, stream); break;
+        case 4: launch_row<T, 4>(a, r, stream); break;
+        case 5: launch_row<T, 5>(a, r, stream); break;
+        case 6: launch_row<T, 6>(a, r, stream); break;
+        case 7: launch_row<T, 7>(a, r, stream); break;
+        default: launch_row<T, 8>(a, r, stream); break;
     }
-    return cudaGetLastError();
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    constexpr int BAND = kWarps * (32 / (DK / 4)) * 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.N * a.HV), (unsigned)((a.dv + BAND - 1) / BAND));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const StepCall s{row, gates, a.d, a.state, a.state_out, a.HK, a.HV, a.dv, (size_t)C};
+    err = cudaLaunchKernelEx(&cfg, ssm_step_kernel<DK, T>, s, static_cast<T *>(a.y));
+    return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
 template <typename T>
@@ -180,6 +224,10 @@ cudaError_t launch_typed(const SsmStepArgs &a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+size_t ssm_step_workspace_bytes(int N, int HK, int HV, int dk, int dv) {
+    return (size_t)N * ((size_t)HV * sizeof(float2) + ((size_t)HV * dv + 2 * (size_t)HK * dk) * sizeof(float));
+}
 
 cudaError_t launch_ssm_step(const SsmStepArgs &a, cudaStream_t stream) {
     return a.dtype == GDN_BF16 ? launch_typed<__nv_bfloat16>(a, stream) : launch_typed<float>(a, stream);

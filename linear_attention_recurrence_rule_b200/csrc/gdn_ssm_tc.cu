@@ -19,8 +19,9 @@
 //  * combine_kernel (gdn_ssm_rows.cu): chains the segments in place; hT.
 //  * scan_kernel, one CTA per (segment, value tile), chunk by chunk: C B^T, the masked
 //    and decayed P, C S^T, P X and the next state, all on tcgen05 with the state in
-//    tensor memory.  Its state only feeds the bf16 y: w_j x_j enters as bf16 hi + lo, S
-//    as one bf16 operand and P as one bf16 operand, each term of y rounded once.
+//    tensor memory.  Its state only feeds the bf16 y: w_j x_j, S and P enter as one
+//    bf16 operand each, so a term of y inside its chunk is rounded once on the way and
+//    one from before it twice.
 //
 // A value tile is 128 columns where it can be: one head of 128, or two heads of 64 of
 // one group, which share C B^T and the loads of b and c; else one head of 64.
@@ -28,8 +29,8 @@
 //
 // scan_kernel's warps: loader (TMA), MMA issuer, table (step sizes, running sums, the
 // factors below), four of 4 warps each -- mask (C B^T -> P in the same tensor memory
-// columns), state (S -> bf16 operand, S times e^{G_L}), weight (w x -> hi + lo pieces of
-// 16 tokens through a ring of 3) and output.  The mask takes e^{G_i-G_j} as the decays
+// columns), state (S -> bf16 operand, S times e^{G_L}), weight (w x, in pieces of 32
+// tokens through a ring of 3) and output.  The mask takes e^{G_i-G_j} as the decays
 // behind j in its 32-token block times those from there to i, both <= 1: one
 // exponential per row and block; only the diagonal blocks take one per element.  All
 // sums of log decays run over the tokens between the two ends (block sums), none is a
@@ -308,6 +309,7 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             const int s = j & 1;
             ok = wt(SB_F0 + s, (uint32_t)((j >> 1) & 1));
             const uint64_t a0 = sdesc_sw128(sb + s * Cfg::STAGE, 16384, 1024);
+#pragma unroll 1
             for (int q = 0; q < 4 && ok; ++q) {
                 const int pc = 4 * j + q, r = pc % 3;
                 ok = wt(SB_WF0 + r, (uint32_t)((pc / 3) & 1));
@@ -372,6 +374,7 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             ok = wt(SB_F0 + s, (uint32_t)((j >> 1) & 1)) && wt(SB_TF0 + s, (uint32_t)((j >> 1) & 1));
             const uint32_t stage = sb + s * Cfg::STAGE;
             const float *tab = reinterpret_cast<const float *>(sm + Cfg::O_TAB + s * NH * 512);
+#pragma unroll 1
             for (int q = 0; q < 4 && ok; ++q) {
                 const int pc = 4 * j + q, r = pc % 3;
                 if (pc >= 3) ok = wt(SB_WE0 + r, (uint32_t)((pc / 3 - 1) & 1));
@@ -447,12 +450,12 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
 template <int VT, int NH>
 struct ScanCfg {
     static constexpr uint32_t XT = VT * 256;
-    static constexpr uint32_t PIECE = VT * 32;               // one bf16 term of 16 tokens
+    static constexpr uint32_t PIECE = VT * 64;               // w x of 32 tokens, bf16
     static constexpr int NS = 3;
     static constexpr uint32_t O_C = 0, O_B = 32768, O_X = O_B + 65536;
     static constexpr uint32_t O_S = O_X + 2 * XT;            // S as bf16: 128 rows (k) x VT
     static constexpr uint32_t O_W = O_S + XT;
-    static constexpr uint32_t O_TAB = O_W + NS * 2 * PIECE;  // [2][NH] x [128]: running sum in the block, delta e^(decay
+    static constexpr uint32_t O_TAB = O_W + NS * PIECE;  // [2][NH] x [128]: running sum in the block, delta e^(decay
                                                              // to its end), delta, w
     static constexpr uint32_t O_BAR = O_TAB + 2 * NH * 2048;
     static constexpr uint32_t BYTES = O_BAR + 512 + 1024;
@@ -586,32 +589,39 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
         for (int c = 0; c < nch && ok; ++c) {
             const uint32_t btile = sb + Cfg::O_B + (c & 1) * 32768, xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
             ok = wt(B_S, (uint32_t)(c & 1));
-            if (ok && c > 0) ok = wt(B_YE, (uint32_t)((c - 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {       // C S^T
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_bf16(tmem + T_Y1, desc_add(cd, (k >> 2) * 16384 + (k & 3) * 32), desc_add(sd, k * 2048), id_cs, k > 0);
-                mma_commit(&bars[B_CE]);
-            }
-            __syncwarp();
-            if (c < last) {          // S^T += B^T (w x)
-                const uint64_t ad = sdesc_sw128(btile, 16384, 1024);
-                for (int q = 0; q < 8 && ok; ++q) {
-                    const int pc = 8 * c + q, r = pc % 3;
-                    ok = wt(B_WF0 + r, (uint32_t)((pc / 3) & 1));
+            // S^T += B^T (w x); between its pieces, when the outputs of the chunk before have
+            // been read, C S^T (it frees the one C tile for the next chunk's load)
+            const uint64_t ad = sdesc_sw128(btile, 16384, 1024);
+#pragma unroll 1
+            for (int q = 0; q < 4 && ok; ++q) {
+                if (q == 2) {
+                    if (c > 0) ok = wt(B_YE, (uint32_t)((c - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t wd = sdesc_sw128(sb + Cfg::O_W + r * 2 * Cfg::PIECE, 2048, 1024);
                     if (elect_one()) {
-                        mma_bf16(tmem + T_S, desc_add(ad, q * 2048), wd, id_up, 1);
-                        mma_bf16(tmem + T_S, desc_add(ad, q * 2048), desc_add(wd, Cfg::PIECE), id_up, 1);
-                        mma_commit(&bars[B_WE0 + r]);
-                        if (q == 7) mma_commit(&bars[B_UD]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16(tmem + T_Y1, desc_add(cd, (k >> 2) * 16384 + (k & 3) * 32), desc_add(sd, k * 2048),
+                                     id_cs, k > 0);
+                        mma_commit(&bars[B_CE]);
                     }
                     __syncwarp();
                 }
+                if (c == last) continue;
+                const int pc = 4 * c + q, r = pc % 3;
+                ok = wt(B_WF0 + r, (uint32_t)((pc / 3) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t wd = sdesc_sw128(sb + Cfg::O_W + r * Cfg::PIECE, 4096, 1024);
+                if (elect_one()) {
+                    mma_bf16(tmem + T_S, desc_add(ad, q * 4096), wd, id_up, 1);
+                    mma_bf16(tmem + T_S, desc_add(ad, q * 4096 + 2048), desc_add(wd, 2048), id_up, 1);
+                    mma_commit(&bars[B_WE0 + r]);
+                    if (q == 3) mma_commit(&bars[B_UD]);
+                }
+                __syncwarp();
             }
             ok = ok && wt(B_P, (uint32_t)(c & 1)) && wt(B_XF0 + (c & 1), par2(c));
             if (!ok) break;
@@ -675,7 +685,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             ok = wt(B_TF0 + (c & 1), par2(c)) && wt(B_CB, (uint32_t)(c & 1));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 const uint32_t ta = tmem_addr(tmem, warp, T_CB + 32 * q);
                 uint32_t out[NH][16];
@@ -690,9 +700,8 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                             // decays of the tokens behind block q, up to i
                             const float *tot = bt + ((c & 1) * NH + e) * 4;
                             float s = pi;
-#pragma unroll
-                            for (int m = 1; m < 3; ++m)
-                                if (m > q && m < w) s += tot[m];
+                            if (q < 1 && w > 1) s += tot[1];
+                            if (q < 2 && w > 2) s += tot[2];
                             const float rf = ex2(s);
                             const float2 rf2 = make_float2(rf, rf);
                             const float4 *cf = reinterpret_cast<const float4 *>(t + 128 + 32 * q);
@@ -749,11 +758,11 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
         }
         tmem_wait_st();
         for (int c = 0; c < nch && ok; ++c) {
-            if (c > 0) ok = wt(B_UD, (uint32_t)((c - 1) & 1));
+            if (c > 0) ok = wt(B_UD, (uint32_t)((c - 1) & 1)) && wt(B_CE, (uint32_t)((c - 1) & 1));
             ok = ok && wt(B_TF0 + (c & 1), par2(c));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int g = 0; g < VT / 32; ++g) {
                 const uint32_t ta = tmem_addr(tmem, warp, T_S + 32 * g);
                 float v[32];
@@ -779,32 +788,35 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             warp_arrive(&bars[B_TE0 + (c & 1)]);
         }
     } else if (warp >= kScWeight && warp < kScOut) {
-        // ------------------------------------------------ w x as hi + lo, 16 tokens a piece
+        // ------------------------------------------------ w x, 32 tokens a piece
         const int tid = threadIdx.x - kScWeight * 32, row = tid >> 3, pc8 = tid & 7;
         for (int c = 0; c < last && ok; ++c) {
             ok = wt(B_XF0 + (c & 1), par2(c)) && wt(B_TF0 + (c & 1), par2(c));
             const uint32_t xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
-            for (int q = 0; q < 8 && ok; ++q) {
-                const int pc = 8 * c + q, r = pc % 3;
+#pragma unroll 1
+            for (int q = 0; q < 4 && ok; ++q) {
+                const int pc = 4 * c + q, r = pc % 3;
                 if (pc >= 3) ok = wt(B_WE0 + r, (uint32_t)((pc / 3 - 1) & 1));
                 if (!ok) break;
-                const int token = 16 * q + row;
+                const uint32_t src = xtile + (32 * q + row) * 128 + pc8 * 16;
+                const uint32_t dst = sb + Cfg::O_W + r * Cfg::PIECE + row * 128 + pc8 * 16;
 #pragma unroll
                 for (int v = 0; v < VT / 64; ++v) {
-                    const uint4 u = lds128(xtile + v * 16384 + token * 128 + pc8 * 16);
-                    const float w = table(c, NH == 2 ? v : 0)[384 + token];
-                    const float2 w2 = make_float2(w, w);
-                    const uint32_t xs[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t hi[4], lo[4];
+                    const float *tab = table(c, NH == 2 ? v : 0) + 384 + 32 * q + row;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float2 f = mulp(unpack2(xs[i]), w2);
-                        hi[i] = take_bf16(f);
-                        lo[i] = pack_bf16x2(f.x, f.y);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint4 u = lds128(src + v * 16384 + half * 2048);
+                        const float w = tab[16 * half];
+                        const float2 w2 = make_float2(w, w);
+                        const uint32_t xs[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = mulp(unpack2(xs[i]), w2);
+                            o[i] = pack_bf16x2(f.x, f.y);
+                        }
+                        sts128(dst + v * 4096 + half * 2048, o[0], o[1], o[2], o[3]);
                     }
-                    const uint32_t dst = sb + Cfg::O_W + r * 2 * Cfg::PIECE + v * 2048 + row * 128 + pc8 * 16;
-                    sts128(dst, hi[0], hi[1], hi[2], hi[3]);
-                    sts128(dst + Cfg::PIECE, lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_proxy_async_smem();
                 warp_arrive(&bars[B_WF0 + r]);
@@ -853,7 +865,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                     if (m < warp - kScOut) s += tot[m];
                 gam[e] = ex2(s);
             }
-#pragma unroll
+#pragma unroll 1
             for (int g = 0; g < VT / 16; ++g) {
                 float v1[16], v2[16];
                 tmem_ld16(tmem_addr(tmem, warp, T_Y1 + 16 * g), v1);
@@ -861,7 +873,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                 const uint32_t xa = xtile + (g >> 2) * 16384;
                 const uint4 xu = lds128(xa + sw128_chunk(i, 2 * (g & 3))), xv = lds128(xa + sw128_chunk(i, 2 * (g & 3) + 1));
                 const uint32_t xw[8] = {xu.x, xu.y, xu.z, xu.w, xv.x, xv.y, xv.z, xv.w};
-                const float ga = gam[(16 * g) / DV], de = dh[(16 * g) / DV];
+                const float ga = NH == 2 && g >= 4 ? gam[NH - 1] : gam[0], de = NH == 2 && g >= 4 ? dh[NH - 1] : dh[0];
                 const float2 ga2 = make_float2(ga, ga), de2 = make_float2(de, de);
                 tmem_wait_ld();
                 uint32_t o[8];

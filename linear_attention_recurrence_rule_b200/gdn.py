@@ -126,7 +126,9 @@ def load_library() -> ctypes.CDLL:
             lib.gdn_ssm_prefill_workspace_size.argtypes = [i32, i64, i32, i32, i32, i32, i32, i32]
             lib.gdn_ssm_step.restype = i32
             lib.gdn_ssm_step.argtypes = [vp] * 9 + [i32, vp, vp, i32, i32, i32, i32, i32, i64, u32,
-                                                    i32, vp, vp]
+                                                    i32, vp, vp, sz, vp]
+            lib.gdn_ssm_step_workspace_size.restype = sz
+            lib.gdn_ssm_step_workspace_size.argtypes = [i32] * 5
             lib.gdn_gated_norm.restype = i32
             lib.gdn_gated_norm.argtypes = [vp, vp, vp, i64, i32, i32, i64, i64, i32, f32, u32, i32,
                                            vp, vp]

@@ -161,9 +161,14 @@ def gdn_ssm_prefill(x, b, c, dt, a, d=None, dt_bias=None, h0=None, cu_seqlens=No
     return y, hT
 
 
+def gdn_ssm_step_workspace_size(N, HK, HV, dk, dv) -> int:
+    """Bytes of workspace ``gdn_ssm_step`` needs."""
+    return int(load_library().gdn_ssm_step_workspace_size(int(N), int(HK), int(HV), int(dk), int(dv)))
+
+
 def gdn_ssm_step(xbc, dt, a, state, d=None, dt_bias=None, conv_weight=None, conv_bias=None,
                  conv_state=None, silu: bool = False, softplus: bool = False, state_out=None,
-                 conv_state_out=None, y=None, stream=None):
+                 conv_state_out=None, y=None, workspace=None, stream=None):
     """One token of the scan for N sequences through ``gdn_ssm_step``.
 
     xbc [N, HV*dv + 2*HK*dk] (a row x | b | c; may be a part of a wider row); dt [N,HV]
@@ -205,10 +210,14 @@ def gdn_ssm_step(xbc, dt, a, state, d=None, dt_bias=None, conv_weight=None, conv
         if y is None:
             y = torch.empty((N, HV, dv), dtype=xbc.dtype, device=dev)
         y_p = _check(y, "y", (N, HV, dv), xbc.dtype, dev)
+        if workspace is None:
+            workspace = torch.empty(lib.gdn_ssm_step_workspace_size(N, HK, HV, dk, dv),
+                                    dtype=torch.uint8, device=dev)
+        ws_p = _check(workspace, "workspace", workspace.shape, workspace.dtype, dev)
         st = lib.gdn_ssm_step(xbc.data_ptr(), dt_p, a_p, d_p, bias_p, w_p, cb_p, cs_p, co_p, W,
                               state_p, out_p, N, HK, HV, dk, dv, row,
                               (SSM_SOFTPLUS if softplus else 0) | (CONV_SILU if silu else 0), code,
-                              y_p, raw)
+                              y_p, ws_p, workspace.numel() * workspace.element_size(), raw)
     if st != GDN_OK:
         raise GDNError(st, "gdn_ssm_step")
     return y

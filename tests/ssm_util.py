@@ -49,13 +49,14 @@ def within(out, ref, allow, what):
 
 def check_scan(y, hT, ref, dtype, tensor_cores, what=""):
     """Bounds: the result's own rounding, the fp32 roundings on the way (doubled, for sums
-    in another order and the hardware exponential), and on the tensor-core path one bf16
-    rounding of each term of y (the decayed scores or the state, whichever carries it)."""
+    in another order and the hardware exponential), and on the tensor-core path two bf16
+    roundings of each term of y (a term inside its chunk one, in its decayed score; one
+    from before it two, in the weighted value and in the state)."""
     r_y, r_h, y_abs, y_units, h_units = ref
     u = U[dtype]
     allow = u * np.abs(r_y) + 2 * U32 * (1 + u) * y_units
     if tensor_cores:
-        allow = allow + U[torch.bfloat16] * (1 + 2.0 ** -6) * y_abs
+        allow = allow + 2 * U[torch.bfloat16] * (1 + 2.0 ** -6) * y_abs
     within(y, r_y, allow + 1e-37, what + "y")
     if hT is not None:
         within(hT, r_h, 2 * U32 * h_units + 1e-37, what + "hT")

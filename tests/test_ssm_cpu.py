@@ -68,7 +68,7 @@ def test_workspace_size_of_rejected_sizes(lib):
 def step(lib, **kw):
     a = dict(xbc=P(0x1000), dt=P(0x2000), a=P(0x3000), d=None, bias=None, w=P(0x4000), cb=None, cs=P(0x5000),
              co=P(0x5000), W=4, state=P(0x6000), out=P(0x6000), N=2, HK=1, HV=2, dk=128, dv=64, row=0, flags=0,
-             dtype=gdn.GDN_BF16, y=P(0x7000))
+             dtype=gdn.GDN_BF16, y=P(0x7000), ws=P(0x8000), wsb=1 << 30)
     assert not set(kw) - set(a)
     a.update(kw)
     return lib.gdn_ssm_step(*a.values(), None)
@@ -91,6 +91,12 @@ def test_step_refusals(lib):
     assert step(lib, xbc=P(0x1001)) == ALIGNMENT
     assert step(lib, w=P(0x4002)) == ALIGNMENT
     assert step(lib, N=0, xbc=None) == OK
+    assert step(lib, N=262141) == UNSUPPORTED
+    need = lib.gdn_ssm_step_workspace_size(2, 1, 2, 128, 64)
+    assert need == 2 * (2 * 8 + (2 * 64 + 2 * 128) * 4)
+    assert step(lib, ws=None) == WORKSPACE and step(lib, wsb=need - 1) == WORKSPACE
+    assert step(lib, ws=P(0x8008)) == ALIGNMENT
+    assert lib.gdn_ssm_step_workspace_size(2, 3, 2, 128, 64) == 0
 
 
 def gated(lib, **kw):
