@@ -28,9 +28,10 @@
 // The state is kept transposed, S^T [dk lanes][value columns].
 //
 // scan_kernel's warps: loader (TMA), MMA issuer, table (step sizes, running sums, the
-// factors below), four of 4 warps each -- mask (C B^T -> P in the same tensor memory
+// factors below), and by groups of 4 warps -- mask (C B^T -> P in the same tensor memory
 // columns), state (S -> bf16 operand, S times e^{G_L}), weight (w x, in pieces of 32
-// tokens through a ring of 3) and output.  The mask takes e^{G_i-G_j} as the decays
+// tokens through a ring of 3) and output
+// (two groups, half of the columns each).  The mask takes e^{G_i-G_j} as the decays
 // behind j in its 32-token block times those from there to i, both <= 1: one
 // exponential per row and block; only the diagonal blocks take one per element.  All
 // sums of log decays run over the tokens between the two ends (block sums), none is a
@@ -71,27 +72,28 @@ struct TcParams {
 };
 
 constexpr long long kWaitCycles = 4000000000LL, kDrainCycles = 100000000LL;
+// The roles' loops share the instruction cache, so what runs seldom is kept out of
+// them: one copy of the polling loop.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *status) {
+    const long long t0 = clock64();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 100000u))) return true;
+        const bool stop = *abort_flag != 0 || clock64() - t0 > kWaitCycles;
+        if (__any_sync(0xffffffffu, stop)) {
+            *abort_flag = 1;
+            atomicExch(status, (unsigned int)GDN_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
 struct Waiter {
     uint64_t *bars;
     volatile int *abort_flag;
     unsigned int *status;
     // false once the CTA has given up (the same in every lane)
-    __device__ bool operator()(int b, uint32_t parity) const {
-        bool ok = mbar_try_wait(&bars[b], parity);
-        if (!__all_sync(0xffffffffu, ok)) {
-            const long long t0 = clock64();
-            for (;;) {
-                ok = mbar_try_wait(&bars[b], parity);
-                if (__all_sync(0xffffffffu, ok)) break;
-                const bool stop = *abort_flag != 0 || clock64() - t0 > kWaitCycles;
-                if (__any_sync(0xffffffffu, stop)) {
-                    *abort_flag = 1;
-                    atomicExch(status, (unsigned int)GDN_ERR_TIMEOUT);
-                    return false;
-                }
-            }
-        }
-        return true;
+    __device__ __forceinline__ bool operator()(int b, uint32_t parity) const {
+        if (__all_sync(0xffffffffu, mbar_try_wait(&bars[b], parity))) return true;
+        return wait_slow(&bars[b], parity, abort_flag, status);
     }
     __device__ void drain(int b, uint32_t parity) const {
         const long long t0 = clock64();
@@ -100,6 +102,12 @@ struct Waiter {
     }
 };
 
+__device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -166,78 +174,88 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
     return w;
 }
 
-// Step sizes and log2 decays of one head's 128 tokens: lane l has tokens 4l .. 4l+3
-// (dt loaded ahead); tokens from `len` on have step size 0.  A log2 decay below -150
-// is taken as -150: every factor with that token in it is 0 in fp32 either way, and
-// the sums of the tokens around it keep their digits.
+// One head's decay and step bias, a * log2 e and dt_bias.
 struct HeadTab {
-    float ah, bias;   // a * log2 e, dt_bias
+    float ah, bias;
 };
-__device__ __forceinline__ void steps4(const float (&dt)[4], const HeadTab &t, int lane, int len, bool soft,
-                                       float (&delta)[4], float (&g)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = 4 * lane + i < len;
-        delta[i] = in ? step_size(dt[i], t.bias, soft) : 0.f;
-        g[i] = in ? fmaxf(delta[i] * t.ah, -150.f) : 0.f;
-    }
+// Step size and log2 decay of a token; no token: both 0.  A log2 decay below -150 is
+// taken as -150: every factor with that token in it is 0 in fp32 either way, and the
+// sums of the tokens around it keep their digits.
+__device__ __forceinline__ void token_step(float dt, const HeadTab &t, bool in, bool soft, float &delta, float &g) {
+    delta = in ? step_size(dt, t.bias, soft) : 0.f;
+    g = in ? fmaxf(delta * t.ah, -150.f) : 0.f;
 }
-__device__ __forceinline__ void load_dt4(const float *dt, int64_t t0, int HV, int h, int lane, int len, float (&v)[4]) {
+// Sums of g inside a 32-token block, a token per lane: `pre` up to and including the
+// token, `suf` behind it; returns the block's sum.  Sums over longer spans add whole
+// blocks to these, so no span's sum is a difference of larger ones.
+__device__ __forceinline__ float block_sums(float g, int lane, float &pre, float &suf) {
+    float up = g, down = g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 4 * lane + i;
-        v[i] = t < len ? __ldg(dt + (t0 + t) * HV + h) : 0.f;
-    }
-}
-// Sums of g inside the 32-token blocks (8 lanes): pre[i] up to and including a token,
-// suf[i] behind it; tot[q] the blocks' totals.  Sums over longer spans add whole blocks
-// to these, so no span's sum is a difference of larger ones.
-__device__ __forceinline__ void block_sums(const float (&g)[4], int lane, float (&pre)[4], float (&suf)[4],
-                                           float (&tot)[4]) {
-    const float own = (g[0] + g[1]) + (g[2] + g[3]);
-    float up = own, down = own;
-#pragma unroll
-    for (int off = 1; off < 8; off <<= 1) {
+    for (int off = 1; off < 32; off <<= 1) {
         const float u = __shfl_up_sync(0xffffffffu, up, off), d = __shfl_down_sync(0xffffffffu, down, off);
-        if ((lane & 7) >= off) up += u;
-        if ((lane & 7) + off < 8) down += d;
+        if (lane >= off) up += u;
+        if (lane + off < 32) down += d;
     }
-    float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
-    if ((lane & 7) == 0) before = 0.f;
-    if ((lane & 7) == 7) after = 0.f;
-    pre[0] = before + g[0];
-    pre[1] = pre[0] + g[1];
-    pre[2] = pre[1] + g[2];
-    pre[3] = pre[2] + g[3];
-    suf[3] = after;
-    suf[2] = after + g[3];
-    suf[1] = suf[2] + g[2];
-    suf[0] = suf[1] + g[1];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) tot[q] = __shfl_sync(0xffffffffu, down, 8 * q);
-}
-// the totals of the blocks behind the lane's own
-__device__ __forceinline__ float blocks_behind(const float (&tot)[4], int lane) {
-    const int q = lane >> 3;
-    return q == 3 ? 0.f : q == 2 ? tot[3] : q == 1 ? tot[2] + tot[3] : (tot[1] + tot[2]) + tot[3];
+    pre = up;
+    suf = __shfl_down_sync(0xffffffffu, down, 1);
+    if (lane == 31) suf = 0.f;
+    return __shfl_sync(0xffffffffu, down, 0);
 }
 
 // -------------------------------------------------------------------- segments' own states
+// S[value][key] += (w x)^T b over the tokens of the segment.  The workers take x^T out of
+// shared memory with transposing matrix loads, weight it and put it into tensor memory as
+// three bf16 terms (the A operand, lanes = value columns): the products then read only b
+// from shared memory, whose bandwidth is what bounds this kernel (with the terms in
+// shared memory it moved 384 KB per 128 tokens of a 128-wide tile instead of 176 KB, and
+// took 280 us instead of XXX us for 64K tokens of 32 heads of 128).  The first terms and
+// the two small ones have an accumulator each, so that the small ones are not rounded
+// away against the large sum, and every kFlush chunks both are added to sums in the
+// workers' registers: the tensor cores truncate, and over the 456 additions of a 7K-token
+// segment the sums fell short by 2.2e-6; over 64 by 3e-7.
 template <int VT, int NH>
 struct StatesCfg {
     static constexpr uint32_t XT = VT * 256;                 // x tile: 128 rows
     static constexpr uint32_t STAGE = 32768 + XT;            // b tile, x tile
-    static constexpr uint32_t TERM = VT * 64;                // one bf16 term of 32 tokens
-    static constexpr int NS = 3;                             // pieces in the ring
-    static constexpr uint32_t O_W = 2 * STAGE;
-    static constexpr uint32_t O_TAB = O_W + NS * 3 * TERM;   // w [2][NH][128]
+    static constexpr int NS = 3;
+    static constexpr uint32_t O_TAB = NS * STAGE;            // w to the chunk's end [2][NH][128]
     static constexpr uint32_t O_BAR = O_TAB + 2 * NH * 512;
     static constexpr uint32_t BYTES = O_BAR + 256 + 1024;
 };
 static_assert(StatesCfg<128, 2>::BYTES <= 232448, "shared memory");
-constexpr int kStWorkers = 8, kStWork0 = 4, kStThreads = (kStWork0 + kStWorkers) * 32;
-enum StBar { SB_F0, SB_F1, SB_E0, SB_E1, SB_TF0, SB_TF1, SB_TE0, SB_TE1, SB_WF0, SB_WE0 = SB_WF0 + 3,
-             SB_DONE = SB_WE0 + 3, SB_COUNT };
+constexpr int kStWorkers = 16, kStWork0 = 4, kStThreads = (kStWork0 + kStWorkers) * 32;
+enum StBar { SB_F0, SB_E0 = SB_F0 + 3, SB_TF0 = SB_E0 + 3, SB_TF1, SB_TE0, SB_TE1, SB_WF0, SB_WF1, SB_WE0, SB_WE1,
+             SB_DONE, SB_READ, SB_END, SB_COUNT };
+constexpr int kFlush = 8;   // chunks between two readings of the accumulators
+// tensor memory: the sums of the first terms, of the small ones, two pieces of 64 tokens
+// (three terms of 32 columns)
+constexpr uint32_t TS_D = 0, TS_DS = 128, TS_A = 256, TS_PIECE = 96;
+
+// four 8x8 blocks of 16-bit elements, each transposed over the warp; lane l gives the
+// address of row l % 8 of block l / 8
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// 16 lanes x 8 columns: registers 2i, 2i + 1 hold columns 4i .. 4i + 3 of lanes l / 4 and
+// l / 4 + 8 (column l % 4 of the four)
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&w)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+// The upper halves of two floats as a bf16 pair (truncated), the floats' remainders left:
+// a 24-bit significand is exactly three such parts.
+__device__ __forceinline__ uint32_t high_pair(float2 x) {
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+__device__ __forceinline__ uint32_t take_high(float2 &x) {
+    const uint32_t w = high_pair(x);
+    x = subp(x, make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                            __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)));
+    return w;
+}
 
 template <int VT, int NH>
 __global__ void __launch_bounds__(kStThreads, 1)
@@ -250,6 +268,7 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::O_BAR);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cfg::O_BAR + 8 * SB_COUNT);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cfg::O_BAR + 8 * SB_COUNT + 4);
+    float *sums = reinterpret_cast<float *>(sm + Cfg::O_BAR + 8 * SB_COUNT + 8);   // log2 decays of a chunk [2][NH]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.HV / NH;
     const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
@@ -257,34 +276,37 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     if (!seg.ok || (seg.last && !p.whole)) return;
     const int nch = (seg.len + L - 1) / L;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&bars[SB_F0 + i], 1);
             mbar_init(&bars[SB_E0 + i], 1 + kStWorkers);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[SB_TF0 + i], 1);
             mbar_init(&bars[SB_TE0 + i], kStWorkers);
-        }
-        for (int i = 0; i < 3; ++i) {
             mbar_init(&bars[SB_WF0 + i], kStWorkers);
             mbar_init(&bars[SB_WE0 + i], 1);
         }
         mbar_init(&bars[SB_DONE], 1);
+        mbar_init(&bars[SB_READ], kStWorkers);
+        mbar_init(&bars[SB_END], 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 3) tmem_alloc(tslot, 128);
+    if (warp == 3) tmem_alloc(tslot, 512);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
     const Waiter wt{bars, abort_flag, p.status};
     auto chunk_of = [&](int j) { return nch - 1 - j; };    // from the end
     auto len_of = [&](int j) { return min(L, seg.len - chunk_of(j) * L); };
+    auto stage_full = [&](int j) { return wt(SB_F0 + j % 3, (uint32_t)((j / 3) & 1)); };
     bool ok = true;
 
     if (warp == 0) {
         int issued = 0;
         for (int j = 0; j < nch; ++j) {
-            const int s = j & 1;
-            if (j >= 2) ok = wt(SB_E0 + s, (uint32_t)(((j >> 1) - 1) & 1));
+            const int s = j % 3;
+            if (j >= 3) ok = wt(SB_E0 + s, (uint32_t)((j / 3 - 1) & 1));
             if (!ok) break;
             if (lane == 0) {
                 uint8_t *st = sm + s * Cfg::STAGE;
@@ -302,147 +324,190 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             __syncwarp();
         }
         // no load stays in flight behind this CTA, whatever the other roles do
-        for (int j = issued > 2 ? issued - 2 : 0; j < issued; ++j) wt.drain(SB_F0 + (j & 1), (uint32_t)((j >> 1) & 1));
+        for (int j = issued > 3 ? issued - 3 : 0; j < issued; ++j) wt.drain(SB_F0 + j % 3, (uint32_t)((j / 3) & 1));
     } else if (warp == 1) {
-        const uint32_t id = idesc_bf16(128, VT, true, true);
+        const uint32_t id = idesc_bf16(128, DK, false, true);
         for (int j = 0; j < nch && ok; ++j) {
-            const int s = j & 1;
-            ok = wt(SB_F0 + s, (uint32_t)((j >> 1) & 1));
-            const uint64_t a0 = sdesc_sw128(sb + s * Cfg::STAGE, 16384, 1024);
+            const bool fresh = j % kFlush == 0;
+            if (fresh && j > 0) ok = wt(SB_READ, (uint32_t)((j / kFlush - 1) & 1));
+            ok = ok && stage_full(j);
+            const uint64_t b0 = sdesc_sw128(sb + (j % 3) * Cfg::STAGE, 16384, 1024);
 #pragma unroll 1
-            for (int q = 0; q < 4 && ok; ++q) {
-                const int pc = 4 * j + q, r = pc % 3;
-                ok = wt(SB_WF0 + r, (uint32_t)((pc / 3) & 1));
+            for (int q = 0; q < 2 && ok; ++q) {
+                const int pc = 2 * j + q, r = pc & 1;
+                ok = wt(SB_WF0 + r, (uint32_t)((pc >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t b0 = sdesc_sw128(sb + Cfg::O_W + r * 3 * Cfg::TERM, 4096, 1024);
                 if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int t = 0; t < 3; ++t)
-                            mma_bf16(tmem, desc_add(a0, q * 4096 + k * 2048), desc_add(b0, t * Cfg::TERM + k * 2048),
-                                     id, pc > 0 || k > 0 || t > 0);
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t bd = desc_add(b0, q * 8192 + k * 2048);
+                        const uint32_t a = tmem + TS_A + r * TS_PIECE + 8 * k;
+                        const uint32_t add = !fresh || q + k > 0;
+                        mma_bf16_ts(tmem + TS_D, a, bd, id, add);
+                        mma_bf16_ts(tmem + TS_DS, a + 32, bd, id, add);
+                        mma_bf16_ts(tmem + TS_DS, a + 64, bd, id, 1);
+                    }
                     mma_commit(&bars[SB_WE0 + r]);
-                    if (q == 3) mma_commit(&bars[SB_E0 + s]);
+                    if (q == 1) mma_commit(&bars[SB_E0 + j % 3]);
+                    if (q == 1 && (j % kFlush == kFlush - 1 || j == nch - 1)) mma_commit(&bars[SB_DONE]);
                 }
                 __syncwarp();
             }
         }
-        if (elect_one()) mma_commit(&bars[SB_DONE]);
+        // every product issued here has completed before tensor memory is released
+        if (elect_one()) mma_commit(&bars[SB_END]);
         __syncwarp();
-        wt.drain(SB_DONE, 0);
-    } else if (warp == 2) {
+        wt.drain(SB_END, 0);
+    } else if (warp == 2 || warp == 3) {
+        // the weights to the chunk's end, every other chunk each
         HeadTab ht[NH];
-        float run[NH], dt[NH][4];
 #pragma unroll
-        for (int e = 0; e < NH; ++e) {
-            ht[e] = {p.a[head + e] * kLog2e, p.dt_bias ? p.dt_bias[head + e] : 0.f};
-            run[e] = 0.f;
-            if (nch > 0) load_dt4(p.dt, seg.t0 + (int64_t)chunk_of(0) * L, p.HV, head + e, lane, len_of(0), dt[e]);
-        }
-        for (int j = 0; j < nch && ok; ++j) {
+        for (int e = 0; e < NH; ++e) ht[e] = {p.a[head + e] * kLog2e, p.dt_bias ? p.dt_bias[head + e] : 0.f};
+        const float *dtp = p.dt + seg.t0 * p.HV + head;
+        auto load_dt = [&](int j, int q, int e) {
+            const int t = chunk_of(j) * L + 32 * q + lane;
+            return t >= 0 && t < seg.len ? __ldg(dtp + (int64_t)t * p.HV + e) : 0.f;
+        };
+        // four blocks of dt on their way, the one used next last
+        const int first = warp - 2;
+        float ahead[NH][4];
+#pragma unroll
+        for (int e = 0; e < NH; ++e)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ahead[e][q] = load_dt(first, q, e);
+        for (int j = first; j < nch && ok; j += 2) {
             const int s = j & 1;
             if (j >= 2) ok = wt(SB_TE0 + s, (uint32_t)(((j >> 1) - 1) & 1));
             if (!ok) break;
+            float *tab = reinterpret_cast<float *>(sm + Cfg::O_TAB + s * NH * 512);
+            float behind[NH];
 #pragma unroll
-            for (int e = 0; e < NH; ++e) {
-                float delta[4], g[4], pre[4], suf[4], tot[4];
-                steps4(dt[e], ht[e], lane, len_of(j), p.soft, delta, g);
-                if (j + 1 < nch) load_dt4(p.dt, seg.t0 + (int64_t)chunk_of(j + 1) * L, p.HV, head + e, lane, L, dt[e]);
-                block_sums(g, lane, pre, suf, tot);
-                const float behind = blocks_behind(tot, lane) + run[e];
-                float4 w;
-                w.x = delta[0] * ex2(suf[0] + behind);
-                w.y = delta[1] * ex2(suf[1] + behind);
-                w.z = delta[2] * ex2(suf[2] + behind);
-                w.w = delta[3] * ex2(suf[3] + behind);
-                reinterpret_cast<float4 *>(sm + Cfg::O_TAB + (s * NH + e) * 512)[lane] = w;
-                run[e] += (tot[0] + tot[1]) + (tot[2] + tot[3]);
+            for (int e = 0; e < NH; ++e) behind[e] = 0.f;
+#pragma unroll 1
+            for (int q = 3; q >= 0; --q) {
+                const bool in = chunk_of(j) * L + 32 * q + lane < seg.len;
+#pragma unroll
+                for (int e = 0; e < NH; ++e) {
+                    float delta, g, pre, suf;
+                    token_step(ahead[e][3], ht[e], in, p.soft, delta, g);
+                    ahead[e][3] = ahead[e][2];
+                    ahead[e][2] = ahead[e][1];
+                    ahead[e][1] = ahead[e][0];
+                    ahead[e][0] = load_dt(j + 2, q, e);
+                    const float sum = block_sums(g, lane, pre, suf);
+                    tab[e * 128 + 32 * q + lane] = delta * ex2(suf + behind[e]);
+                    behind[e] += sum;
+                }
             }
+            if (lane < NH) sums[s * NH + lane] = NH == 2 && lane == 1 ? behind[NH - 1] : behind[0];
             warp_arrive(&bars[SB_TF0 + s]);
         }
-        if (lane < NH) {
-            float r = run[0];
-            if (NH == 2 && lane == 1) r = run[NH - 1];
-            p.seg_decay[(size_t)slot * p.HV + head + lane] = ex2(r);
-        }
     } else if (warp >= kStWork0) {
-        const int tid = threadIdx.x - kStWork0 * 32, row = tid >> 3, pc8 = tid & 7;
+        // lanes (value columns) 32 quad .. + 31; tokens 16 th .. + 15 of every piece, and
+        // columns 32 th .. + 31 of the sums
+        const int quad = warp & 3, th = (warp - kStWork0) >> 2, tid = threadIdx.x - kStWork0 * 32;
+        const bool mine = 32 * quad < VT;                       // (a tile of 64 fills half of the lanes)
+        const int e = NH == 2 ? quad >> 1 : 0;
+        // this lane's row of the 8x8 blocks: token (lane & 7) + 8 of blocks 2, 3; columns + 8 of blocks 1, 3
+        const int trow = 16 * th + (lane & 7) + 8 * (lane >> 4), vblk = (lane >> 3) & 1;
+        float run[NH], acc[32];      // log2 decays behind the chunk; the sums
+#pragma unroll
+        for (int h = 0; h < NH; ++h) run[h] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[i] = 0.f;
         for (int j = 0; j < nch && ok; ++j) {
             const int s = j & 1, len = len_of(j);
-            ok = wt(SB_F0 + s, (uint32_t)((j >> 1) & 1)) && wt(SB_TF0 + s, (uint32_t)((j >> 1) & 1));
-            const uint32_t stage = sb + s * Cfg::STAGE;
-            const float *tab = reinterpret_cast<const float *>(sm + Cfg::O_TAB + s * NH * 512);
-#pragma unroll 1
-            for (int q = 0; q < 4 && ok; ++q) {
-                const int pc = 4 * j + q, r = pc % 3;
-                if (pc >= 3) ok = wt(SB_WE0 + r, (uint32_t)((pc / 3 - 1) & 1));
-                if (!ok) break;
-                const int token = 32 * q + row;
-                const bool in = token < len;
-                const uint32_t dst0 = sb + Cfg::O_W + r * 3 * Cfg::TERM + row * 128 + pc8 * 16;
+            ok = stage_full(j) && wt(SB_TF0 + s, (uint32_t)((j >> 1) & 1));
+            if (!ok) break;
+            const uint32_t stage = sb + (j % 3) * Cfg::STAGE;
+            const float *tab = reinterpret_cast<const float *>(sm + Cfg::O_TAB + (s * NH + e) * 512);
+            const float far = ex2(NH == 2 && e == 1 ? run[NH - 1] : run[0]);
 #pragma unroll
-                for (int v = 0; v < VT / 64; ++v) {
-                    uint32_t hi[4] = {0, 0, 0, 0}, mid[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-                    if (in) {
-                        const uint4 u = lds128(stage + 32768 + v * 16384 + token * 128 + pc8 * 16);
-                        const float w = tab[(NH == 2 ? v : 0) * 128 + token];
-                        const float2 w2 = make_float2(w, w);
-                        const uint32_t xs[4] = {u.x, u.y, u.z, u.w};
+            for (int h = 0; h < NH; ++h) run[h] += sums[s * NH + h];
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                const int pc = 2 * j + q, r = pc & 1;
+                if (pc >= 2) ok = wt(SB_WE0 + r, (uint32_t)(((pc >> 1) - 1) & 1));
+                if (!ok) break;
+                if (mine) {
+                    const int tok = 64 * q + 16 * th + 2 * (lane & 3);   // + 8 i + {0, 1}
+                    float2 w2[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        w2[i] = *reinterpret_cast<const float2 *>(tab + tok + 8 * i);
+                        w2[i] = mulp(w2[i], make_float2(far, far));
+                    }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int col = 32 * quad + 16 * g + 8 * vblk;
+                        uint32_t x[4], hi[4], mid[4], lo[4];
+                        ldsm_x4_t(stage + 32768 + (col >> 6) * 16384 + sw128_chunk(64 * q + trow, (col & 63) >> 3), x);
+                        if (len < L) {   // rows behind the sequence may hold anything
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int t = tok + 8 * (i >> 1);
+                                if (t >= len) x[i] = 0u;
+                                if (t + 1 >= len) x[i] &= 0xffffu;
+                            }
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float2 f = mulp(unpack2(xs[i]), w2);
-                            hi[i] = take_bf16(f);
-                            mid[i] = take_bf16(f);
-                            lo[i] = pack_bf16x2(f.x, f.y);
+                            float2 f = mulp(unpack2(x[i]), w2[i >> 1]);
+                            hi[i] = take_high(f);
+                            mid[i] = take_high(f);
+                            lo[i] = high_pair(f);
                         }
+                        const uint32_t ta = tmem + ((uint32_t)(32 * quad + 16 * g) << 16) + TS_A + r * TS_PIECE + 8 * th;
+                        tmem_st_16x128b_x2(ta, hi);
+                        tmem_st_16x128b_x2(ta + 32, mid);
+                        tmem_st_16x128b_x2(ta + 64, lo);
                     }
-                    const uint32_t dst = dst0 + v * 4096;
-                    sts128(dst, hi[0], hi[1], hi[2], hi[3]);
-                    sts128(dst + Cfg::TERM, mid[0], mid[1], mid[2], mid[3]);
-                    sts128(dst + 2 * Cfg::TERM, lo[0], lo[1], lo[2], lo[3]);
+                    tmem_wait_st();
                 }
-                if (!in) {
-                    // another sequence's rows (or none): a NaN there must not meet the zeros
-                    sts128(stage + token * 128 + pc8 * 16, 0, 0, 0, 0);
-                    sts128(stage + 16384 + token * 128 + pc8 * 16, 0, 0, 0, 0);
+                if (len < L) {
+                    // rows of b behind the sequence: a NaN there must not meet the zeros
+                    for (int v = tid; v < 64 * 16; v += kStWorkers * 32) {
+                        const int row = 64 * q + (v >> 4), ch = v & 15;
+                        if (row >= len) sts128(stage + (ch >> 3) * 16384 + row * 128 + (ch & 7) * 16, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
+                tc_fence_before();
                 warp_arrive(&bars[SB_WF0 + r]);
             }
-            if (ok) {
-                warp_arrive(&bars[SB_E0 + s]);
-                warp_arrive(&bars[SB_TE0 + s]);
+            if (!ok) break;
+            warp_arrive(&bars[SB_E0 + j % 3]);
+            warp_arrive(&bars[SB_TE0 + s]);
+            if (j % kFlush == kFlush - 1 || j == nch - 1) {
+                ok = wt(SB_DONE, (uint32_t)((j / kFlush) & 1));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float hi[16], small[16];
+                    tmem_ld16(tmem_addr(tmem, warp, TS_D + 32 * th + 16 * g), hi);
+                    tmem_ld16(tmem_addr(tmem, warp, TS_DS + 32 * th + 16 * g), small);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[16 * g + i] += hi[i] + small[i];
+                }
+                tc_fence_before();
+                warp_arrive(&bars[SB_READ]);
             }
         }
-        ok = ok && wt(SB_DONE, 0);
-        if (ok) {
-            tc_fence_after();
-            // lane quadrant warp % 4 (key indices), half of the columns
-            const int wq = warp - kStWork0, half = wq >> 2, k = 32 * (warp & 3) + lane;
+        if (ok && tid < NH) p.seg_decay[(size_t)slot * p.HV + head + tid] = ex2(NH == 2 && tid == 1 ? run[NH - 1] : run[0]);
+        if (ok && mine) {
+            const int v = 32 * quad + lane, h = head + v / DV;
+            float4 *dst = reinterpret_cast<float4 *>(p.seg_state + (((size_t)slot * p.HV + h) * DV + v % DV) * DK + 32 * th);
 #pragma unroll
-            for (int g = 0; g < VT / 64; ++g) {
-                const int col = half * (VT / 2) + 32 * g;
-                float v[32];
-                if (nch > 0) {
-                    tmem_ld32r(tmem_addr(tmem, warp, col), v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                }
-                const int h = head + col / DV;
-                float *dst = p.seg_state + (((size_t)slot * p.HV + h) * DV + col % DV) * DK + k;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) dst[i * DK] = v[i];
-            }
-            tc_fence_before();
+            for (int u = 0; u < 8; ++u) dst[u] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
         }
     }
     __syncthreads();
     if (warp == 3) {
         tc_fence_after();
-        tmem_dealloc(tmem, 128);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -455,16 +520,25 @@ struct ScanCfg {
     static constexpr uint32_t O_C = 0, O_B = 32768, O_X = O_B + 65536;
     static constexpr uint32_t O_S = O_X + 2 * XT;            // S as bf16: 128 rows (k) x VT
     static constexpr uint32_t O_W = O_S + XT;
-    static constexpr uint32_t O_TAB = O_W + NS * PIECE;  // [2][NH] x [128]: running sum in the block, delta e^(decay
-                                                             // to its end), delta, w
-    static constexpr uint32_t O_BAR = O_TAB + 2 * NH * 2048;
-    static constexpr uint32_t BYTES = O_BAR + 512 + 1024;
+    static constexpr int NT = 3;                             // table buffers
+    static constexpr uint32_t O_TAB = O_W + NS * PIECE;      // [NT][NH] x HeadTable
+    static constexpr uint32_t O_BAR = O_TAB + NT * NH * 1536;
+    static constexpr uint32_t BYTES = O_BAR + 768 + 1024;
 };
 static_assert(ScanCfg<128, 2>::BYTES <= 232448, "shared memory");
-constexpr int kScMask = 4, kScState = 8, kScWeight = 12, kScOut = 16, kScThreads = 20 * 32;
-enum ScBar { B_CF, B_CE, B_BF0, B_BF1, B_BE0, B_BE1, B_XF0, B_XF1, B_XE0, B_XE1, B_TF0, B_TF1, B_TE0, B_TE1,
-             B_CB, B_P, B_S, B_UD, B_WF0, B_WE0 = B_WF0 + 3, B_Y = B_WE0 + 3, B_YE, B_CL, B_DONE, B_COUNT };
+constexpr int kScMask = 4, kScState = 8, kScWeight = 12, kScOut = 16, kScThreads = 24 * 32;
+enum ScBar { B_CF, B_CE, B_BF0, B_BF1, B_BE0, B_BE1, B_XF0, B_XF1, B_XE0, B_XE1, B_TF0, B_TE0 = B_TF0 + 3,
+             B_CB = B_TE0 + 3, B_P, B_S, B_UD, B_WF0, B_WE0 = B_WF0 + 3, B_Y = B_WE0 + 3, B_YE, B_CL, B_DONE, B_COUNT };
 static_assert(8 * B_COUNT + 8 <= 384, "barriers");
+// One head's factors of a chunk: per token the running sum of log2 decays in its
+// 32-token block, delta times the decays behind it in the block, and delta; per block
+// the sum of its log2 decays and the decays behind the block.
+struct HeadTable {
+    float run[L], tail[L], delta[L];
+};
+struct BlockTable {
+    float sum[4], behind[4], all;   // (all: the decays of the whole chunk)
+};
 constexpr uint32_t T_CB = 0, T_Y1 = 128, T_Y2 = 256, T_S = 384;
 
 template <int VT, int NH>
@@ -479,8 +553,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::O_BAR);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cfg::O_BAR + 8 * B_COUNT);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cfg::O_BAR + 8 * B_COUNT + 4);
-    float *bt = reinterpret_cast<float *>(sm + Cfg::O_BAR + 384);   // block totals [2][NH][4]
-    float *gl = bt + 16;                                            // e^{G_L} [2][NH]
+    BlockTable *blocks = reinterpret_cast<BlockTable *>(sm + Cfg::O_BAR + 384);   // [NT][NH]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.HV / NH;
     const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
@@ -495,9 +568,11 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             mbar_init(&bars[B_BF0 + i], 1);
             mbar_init(&bars[B_BE0 + i], 1);
             mbar_init(&bars[B_XF0 + i], 1);
-            mbar_init(&bars[B_XE0 + i], 8);
+            mbar_init(&bars[B_XE0 + i], 12);
+        }
+        for (int i = 0; i < Cfg::NT; ++i) {
             mbar_init(&bars[B_TF0 + i], 1);
-            mbar_init(&bars[B_TE0 + i], 16);
+            mbar_init(&bars[B_TE0 + i], 20);
         }
         mbar_init(&bars[B_CB], 1);
         mbar_init(&bars[B_P], 4);
@@ -508,7 +583,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             mbar_init(&bars[B_WE0 + i], 1);
         }
         mbar_init(&bars[B_Y], 1);
-        mbar_init(&bars[B_YE], 4);
+        mbar_init(&bars[B_YE], 8);
         mbar_init(&bars[B_CL], 4);
         mbar_init(&bars[B_DONE], 1);
         *abort_flag = 0;
@@ -521,7 +596,9 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
     const Waiter wt{bars, abort_flag, p.status};
     auto par2 = [](int c) { return (uint32_t)((c >> 1) & 1); };          // phase of use c >> 1 (two buffers)
     auto par2_before = [](int c) { return (uint32_t)(((c >> 1) - 1) & 1); };
-    auto table = [&](int c, int e) { return reinterpret_cast<float *>(sm + Cfg::O_TAB + ((c & 1) * NH + e) * 2048); };
+    auto table = [&](int c, int e) { return reinterpret_cast<HeadTable *>(sm + Cfg::O_TAB + ((c % 3) * NH + e) * 1536); };
+    auto block = [&](int c, int e) { return blocks + (c % 3) * NH + e; };
+    auto table_full = [&](int c) { return wt(B_TF0 + c % 3, (uint32_t)((c / 3) & 1)); };
     bool ok = true;
 
     if (warp == 0) {
@@ -530,6 +607,17 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
         for (int c = 0; c < nch; ++c) {
             const int s = c & 1, t = (int)(seg.t0 + (int64_t)c * L);
             const int gb = head / (p.HV / p.HK) * DK;
+            // the tiles' slots come free late: what they take next is in L2 by then
+            if (lane == 0 && c + 2 < nch) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    tma_prefetch_l2_2d(&tm_b, gb + 64 * q, t + 2 * L);
+                    tma_prefetch_l2_2d(&tm_c, gb + 64 * q, t + 2 * L);
+                }
+#pragma unroll
+                for (int q = 0; q < VT / 64; ++q) tma_prefetch_l2_2d(&tm_x, head * DV + 64 * q, t + 2 * L);
+            }
+            __syncwarp();
             if (c >= 2) ok = wt(B_BE0 + s, par2_before(c));
             if (!ok) break;
             if (lane == 0) {
@@ -576,7 +664,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             tc_fence_after();
             const uint64_t bd = sdesc_sw128(sb + Cfg::O_B + (c & 1) * 32768, 16, 1024);
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
                     mma_bf16(tmem + T_CB, desc_add(cd, off), desc_add(bd, off), id_cb, k > 0);
@@ -601,7 +689,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < 8; ++k)
                             mma_bf16(tmem + T_Y1, desc_add(cd, (k >> 2) * 16384 + (k & 3) * 32), desc_add(sd, k * 2048),
                                      id_cs, k > 0);
@@ -630,7 +718,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
 #pragma unroll
                 for (int e = 0; e < NH; ++e) {
                     const uint64_t xd = sdesc_sw128(xtile + e * 16384, 16384, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 8; ++k)
                         mma_bf16_ts(tmem + T_Y2 + DV * e, tmem + T_CB + 32 * (k >> 1) + 8 * (k & 1) + 16 * e,
                                     desc_add(xd, k * 2048), id_px, k > 0);
@@ -644,104 +732,118 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
         if (elect_one()) mma_commit(&bars[B_DONE]);
         __syncwarp();
         wt.drain(B_DONE, 0);
-    } else if (warp == 2) {
-        // ------------------------------------------------ tables
+    } else if (warp == 2 || warp == 3) {
+        // ------------------------------------------------ tables (every other chunk each)
         HeadTab ht[NH];
-        float dt[NH][4];
-        auto len_of = [&](int c) { return c == last ? tail : L; };
 #pragma unroll
-        for (int e = 0; e < NH; ++e) {
-            ht[e] = {p.a[head + e] * kLog2e, p.dt_bias ? p.dt_bias[head + e] : 0.f};
-            load_dt4(p.dt, seg.t0, p.HV, head + e, lane, len_of(0), dt[e]);
-        }
-        for (int c = 0; c < nch && ok; ++c) {
-            if (c >= 2) ok = wt(B_TE0 + (c & 1), par2_before(c));
+        for (int e = 0; e < NH; ++e) ht[e] = {p.a[head + e] * kLog2e, p.dt_bias ? p.dt_bias[head + e] : 0.f};
+        const float *dtp = p.dt + seg.t0 * p.HV + head;
+        auto load_dt = [&](int c, int q, int e) {
+            const int t = c * L + 32 * q + lane;
+            return t < seg.len ? __ldg(dtp + (int64_t)t * p.HV + e) : 0.f;
+        };
+        // four blocks of dt on their way, the one used next last
+        const int first = warp - 2;
+        float ahead[NH][4];
+#pragma unroll
+        for (int e = 0; e < NH; ++e)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ahead[e][q] = load_dt(first, q, e);
+        for (int c = first; c < nch && ok; c += 2) {
+            if (c >= 3) ok = wt(B_TE0 + c % 3, (uint32_t)((c / 3 - 1) & 1));
             if (!ok) break;
+            float behind[NH];
 #pragma unroll
-            for (int e = 0; e < NH; ++e) {
-                float delta[4], g[4], pre[4], suf[4], tot[4];
-                steps4(dt[e], ht[e], lane, len_of(c), p.soft, delta, g);
-                if (c < last) load_dt4(p.dt, seg.t0 + (int64_t)(c + 1) * L, p.HV, head + e, lane, len_of(c + 1), dt[e]);
-                block_sums(g, lane, pre, suf, tot);
-                const float behind = blocks_behind(tot, lane);
-                float4 *t = reinterpret_cast<float4 *>(table(c, e));
-                t[lane] = make_float4(pre[0], pre[1], pre[2], pre[3]);
-                t[32 + lane] = make_float4(delta[0] * ex2(suf[0]), delta[1] * ex2(suf[1]), delta[2] * ex2(suf[2]),
-                                           delta[3] * ex2(suf[3]));
-                t[64 + lane] = make_float4(delta[0], delta[1], delta[2], delta[3]);
-                t[96 + lane] = make_float4(delta[0] * ex2(suf[0] + behind), delta[1] * ex2(suf[1] + behind),
-                                           delta[2] * ex2(suf[2] + behind), delta[3] * ex2(suf[3] + behind));
-                if (lane == 0) {
-                    gl[(c & 1) * NH + e] = ex2((tot[0] + tot[1]) + (tot[2] + tot[3]));
-                    *reinterpret_cast<float4 *>(bt + ((c & 1) * NH + e) * 4) = make_float4(tot[0], tot[1], tot[2], tot[3]);
+            for (int e = 0; e < NH; ++e) behind[e] = 0.f;
+#pragma unroll 1
+            for (int q = 3; q >= 0; --q) {
+                const bool in = c * L + 32 * q + lane < seg.len;
+#pragma unroll
+                for (int e = 0; e < NH; ++e) {
+                    float delta, g, pre, suf;
+                    token_step(ahead[e][3], ht[e], in, p.soft, delta, g);
+                    ahead[e][3] = ahead[e][2];
+                    ahead[e][2] = ahead[e][1];
+                    ahead[e][1] = ahead[e][0];
+                    ahead[e][0] = load_dt(c + 2, q, e);
+                    const float sum = block_sums(g, lane, pre, suf);
+                    HeadTable *tab = table(c, e);
+                    tab->run[32 * q + lane] = pre;
+                    tab->tail[32 * q + lane] = delta * ex2(suf);
+                    tab->delta[32 * q + lane] = delta;
+                    if (lane == 0) {
+                        block(c, e)->sum[q] = sum;
+                        block(c, e)->behind[q] = ex2(behind[e]);
+                    }
+                    behind[e] += sum;
+                    if (q == 0 && lane == 0) block(c, e)->all = ex2(behind[e]);
                 }
             }
-            warp_arrive(&bars[B_TF0 + (c & 1)]);
+            warp_arrive(&bars[B_TF0 + c % 3]);
         }
     } else if (warp >= kScMask && warp < kScState) {
         // ------------------------------------------------ mask: C B^T -> P (rows i = tokens)
         const int w = warp - kScMask, i = 32 * w + lane;
         for (int c = 0; c < nch && ok; ++c) {
-            ok = wt(B_TF0 + (c & 1), par2(c)) && wt(B_CB, (uint32_t)(c & 1));
+            ok = table_full(c) && wt(B_CB, (uint32_t)(c & 1));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 const uint32_t ta = tmem_addr(tmem, warp, T_CB + 32 * q);
-                uint32_t out[NH][16];
-                if (q <= w) {
-                    float v[32];
-                    tmem_ld32r(ta, v);
+                uint32_t out[16];
+                if (q > w) {
 #pragma unroll
-                    for (int e = 0; e < NH; ++e) {
-                        const float *t = table(c, e);
-                        const float pi = t[i];
-                        if (q < w) {
-                            // decays of the tokens behind block q, up to i
-                            const float *tot = bt + ((c & 1) * NH + e) * 4;
-                            float s = pi;
-                            if (q < 1 && w > 1) s += tot[1];
-                            if (q < 2 && w > 2) s += tot[2];
-                            const float rf = ex2(s);
-                            const float2 rf2 = make_float2(rf, rf);
-                            const float4 *cf = reinterpret_cast<const float4 *>(t + 128 + 32 * q);
+                    for (int u = 0; u < 16; ++u) out[u] = 0u;
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const float4 f = cf[u];
-                                const float2 p0 = mulp(mulp(make_float2(f.x, f.y), rf2), make_float2(v[4 * u], v[4 * u + 1]));
-                                const float2 p1 = mulp(mulp(make_float2(f.z, f.w), rf2), make_float2(v[4 * u + 2], v[4 * u + 3]));
-                                out[e][2 * u] = pack_bf16x2(p0.x, p0.y);
-                                out[e][2 * u + 1] = pack_bf16x2(p1.x, p1.y);
-                            }
-                        } else {
-                            const float4 *pj = reinterpret_cast<const float4 *>(t + 32 * q);
-                            const float4 *dj = reinterpret_cast<const float4 *>(t + 256 + 32 * q);
+                    for (int e = 0; e < NH; ++e) tmem_st16w(ta + 16 * e, out);
+                    continue;
+                }
+                float v[32];
+                tmem_ld32r(ta, v);
+#pragma unroll 1
+                for (int e = 0; e < NH; ++e) {
+                    const HeadTable *t = table(c, e);
+                    const float pi = t->run[i];
+                    if (q < w) {
+                        // decays of the tokens behind block q, up to i
+                        const BlockTable *b = block(c, e);
+                        float s = pi;
+                        if (q < 1 && w > 1) s += b->sum[1];
+                        if (q < 2 && w > 2) s += b->sum[2];
+                        const float rf = ex2(s);
+                        const float2 rf2 = make_float2(rf, rf);
+                        const float4 *cf = reinterpret_cast<const float4 *>(t->tail + 32 * q);
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const float4 g4 = pj[u], d4 = dj[u];
-                                const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
-                                float f[4];
+                        for (int u = 0; u < 8; ++u) {
+                            const float4 f = cf[u];
+                            const float2 p0 = mulp(mulp(make_float2(f.x, f.y), rf2), make_float2(v[4 * u], v[4 * u + 1]));
+                            const float2 p1 = mulp(mulp(make_float2(f.z, f.w), rf2), make_float2(v[4 * u + 2], v[4 * u + 3]));
+                            out[2 * u] = pack_bf16x2(p0.x, p0.y);
+                            out[2 * u + 1] = pack_bf16x2(p1.x, p1.y);
+                        }
+                    } else {
+                        const float4 *pj = reinterpret_cast<const float4 *>(t->run + 32 * q);
+                        const float4 *dj = reinterpret_cast<const float4 *>(t->delta + 32 * q);
 #pragma unroll
-                                for (int b = 0; b < 4; ++b)
-                                    f[b] = 4 * u + b <= lane ? v[4 * u + b] * (ds[b] * ex2(pi - gs[b])) : 0.f;
-                                out[e][2 * u] = pack_bf16x2(f[0], f[1]);
-                                out[e][2 * u + 1] = pack_bf16x2(f[2], f[3]);
-                            }
+                        for (int u = 0; u < 8; ++u) {
+                            const float4 g4 = pj[u], d4 = dj[u];
+                            const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
+                            float f[4];
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                f[b] = 4 * u + b <= lane ? v[4 * u + b] * (ds[b] * ex2(pi - gs[b])) : 0.f;
+                            out[2 * u] = pack_bf16x2(f[0], f[1]);
+                            out[2 * u + 1] = pack_bf16x2(f[2], f[3]);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < NH; ++e)
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) out[e][u] = 0u;
+                    tmem_st16w(ta + 16 * e, out);
                 }
-#pragma unroll
-                for (int e = 0; e < NH; ++e) tmem_st16w(ta + 16 * e, out[e]);
             }
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bars[B_P]);
-            warp_arrive(&bars[B_TE0 + (c & 1)]);
+            warp_arrive(&bars[B_TE0 + c % 3]);
         }
     } else if (warp >= kScState && warp < kScWeight) {
         // ------------------------------------------------ state (lanes k)
@@ -759,7 +861,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
         tmem_wait_st();
         for (int c = 0; c < nch && ok; ++c) {
             if (c > 0) ok = wt(B_UD, (uint32_t)((c - 1) & 1)) && wt(B_CE, (uint32_t)((c - 1) & 1));
-            ok = ok && wt(B_TF0 + (c & 1), par2(c));
+            ok = ok && table_full(c);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -774,7 +876,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                            pack_bf16x2(v[8 * u + 2], v[8 * u + 3]), pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
                            pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
                 if (c < last) {
-                    const float s = gl[(c & 1) * NH + (32 * g) / DV];
+                    const float s = block(c, (32 * g) / DV)->all;
                     uint32_t o[32];
 #pragma unroll
                     for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(v[u] * s);
@@ -785,13 +887,13 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&bars[B_S]);
-            warp_arrive(&bars[B_TE0 + (c & 1)]);
+            warp_arrive(&bars[B_TE0 + c % 3]);
         }
     } else if (warp >= kScWeight && warp < kScOut) {
         // ------------------------------------------------ w x, 32 tokens a piece
         const int tid = threadIdx.x - kScWeight * 32, row = tid >> 3, pc8 = tid & 7;
         for (int c = 0; c < last && ok; ++c) {
-            ok = wt(B_XF0 + (c & 1), par2(c)) && wt(B_TF0 + (c & 1), par2(c));
+            ok = wt(B_XF0 + (c & 1), par2(c)) && table_full(c);
             const uint32_t xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
 #pragma unroll 1
             for (int q = 0; q < 4 && ok; ++q) {
@@ -802,11 +904,12 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                 const uint32_t dst = sb + Cfg::O_W + r * Cfg::PIECE + row * 128 + pc8 * 16;
 #pragma unroll
                 for (int v = 0; v < VT / 64; ++v) {
-                    const float *tab = table(c, NH == 2 ? v : 0) + 384 + 32 * q + row;
+                    const float *tab = table(c, NH == 2 ? v : 0)->tail + 32 * q + row;
+                    const float behind = block(c, NH == 2 ? v : 0)->behind[q];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint4 u = lds128(src + v * 16384 + half * 2048);
-                        const float w = tab[16 * half];
+                        const float w = tab[16 * half] * behind;
                         const float2 w2 = make_float2(w, w);
                         const uint32_t xs[4] = {u.x, u.y, u.z, u.w};
                         uint32_t o[4];
@@ -823,7 +926,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             }
             if (ok) {
                 warp_arrive(&bars[B_XE0 + (c & 1)]);
-                warp_arrive(&bars[B_TE0 + (c & 1)]);
+                warp_arrive(&bars[B_TE0 + c % 3]);
             }
         }
         if (tail < L && ok) {
@@ -844,44 +947,44 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
         }
     } else if (warp >= kScOut) {
         // ------------------------------------------------ y (rows i = tokens)
-        const int i = 32 * (warp - kScOut) + lane;
-        float dh[NH];
-#pragma unroll
-        for (int e = 0; e < NH; ++e) dh[e] = p.d ? p.d[head + e] : 0.f;
+        // half of the columns each: with two heads, a head each
+        const int quad = warp & 3, half = (warp - kScOut) >> 2, i = 32 * quad + lane;
+        const int e = NH == 2 ? half : 0, col0 = half * (VT / 2);
+        const float dh = p.d ? p.d[head + e] : 0.f;
+        const float2 de2 = make_float2(dh, dh);
+        __nv_bfloat16 *yr = p.y + ((seg.t0 + i) * p.HV + head) * DV + col0;
         for (int c = 0; c < nch && ok; ++c) {
-            ok = wt(B_TF0 + (c & 1), par2(c)) && wt(B_XF0 + (c & 1), par2(c)) && wt(B_Y, (uint32_t)(c & 1));
+            ok = table_full(c) && wt(B_XF0 + (c & 1), par2(c));
+            if (!ok) break;
+            float s = table(c, e)->run[i];
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+                if (m < quad) s += block(c, e)->sum[m];
+            const float ga = ex2(s);
+            const float2 ga2 = make_float2(ga, ga);
+            warp_arrive(&bars[B_TE0 + c % 3]);
+            ok = wt(B_Y, (uint32_t)(c & 1));
             if (!ok) break;
             tc_fence_after();
             const bool in = c < last || i < tail;
             const uint32_t xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
-            __nv_bfloat16 *yr = p.y + ((seg.t0 + (int64_t)c * L + i) * p.HV + head) * DV;
-            float gam[NH];
-#pragma unroll
-            for (int e = 0; e < NH; ++e) {
-                const float *tot = bt + ((c & 1) * NH + e) * 4;
-                float s = table(c, e)[i];
-#pragma unroll
-                for (int m = 0; m < 3; ++m)
-                    if (m < warp - kScOut) s += tot[m];
-                gam[e] = ex2(s);
-            }
 #pragma unroll 1
-            for (int g = 0; g < VT / 16; ++g) {
+            for (int g = 0; g < VT / 32; ++g) {
+                const int col = col0 + 16 * g;
                 float v1[16], v2[16];
-                tmem_ld16(tmem_addr(tmem, warp, T_Y1 + 16 * g), v1);
-                tmem_ld16(tmem_addr(tmem, warp, T_Y2 + 16 * g), v2);
-                const uint32_t xa = xtile + (g >> 2) * 16384;
-                const uint4 xu = lds128(xa + sw128_chunk(i, 2 * (g & 3))), xv = lds128(xa + sw128_chunk(i, 2 * (g & 3) + 1));
+                tmem_ld16(tmem_addr(tmem, warp, T_Y1 + col), v1);
+                tmem_ld16(tmem_addr(tmem, warp, T_Y2 + col), v2);
+                const uint32_t xa = xtile + (col >> 6) * 16384;
+                const int ch = (col & 63) >> 3;
+                const uint4 xu = lds128(xa + sw128_chunk(i, ch)), xv = lds128(xa + sw128_chunk(i, ch + 1));
                 const uint32_t xw[8] = {xu.x, xu.y, xu.z, xu.w, xv.x, xv.y, xv.z, xv.w};
-                const float ga = NH == 2 && g >= 4 ? gam[NH - 1] : gam[0], de = NH == 2 && g >= 4 ? dh[NH - 1] : dh[0];
-                const float2 ga2 = make_float2(ga, ga), de2 = make_float2(de, de);
                 tmem_wait_ld();
                 uint32_t o[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    float2 s = fma2(ga2, make_float2(v1[2 * u], v1[2 * u + 1]), make_float2(v2[2 * u], v2[2 * u + 1]));
-                    s = fma2(de2, unpack2(xw[u]), s);
-                    o[u] = pack_bf16x2(s.x, s.y);
+                    float2 f = fma2(ga2, make_float2(v1[2 * u], v1[2 * u + 1]), make_float2(v2[2 * u], v2[2 * u + 1]));
+                    f = fma2(de2, unpack2(xw[u]), f);
+                    o[u] = pack_bf16x2(f.x, f.y);
                 }
                 if (in) {
                     if (p.wide_store) {
@@ -897,7 +1000,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             tc_fence_before();
             warp_arrive(&bars[B_YE]);
             warp_arrive(&bars[B_XE0 + (c & 1)]);
-            warp_arrive(&bars[B_TE0 + (c & 1)]);
+            yr += (size_t)L * p.HV * DV;
         }
     }
     __syncthreads();
@@ -968,7 +1071,8 @@ cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     const bool cuts = packed ? a.T > cut.seg_len : cut.nseg > 1;
     const bool states = cuts || a.hT != nullptr;
-    TcParams p{a.dt, a.a, a.d, a.dt_bias, a.h0, a.HK, a.HV, a.softplus, static_cast<__nv_bfloat16 *>(a.y),
+    TcParams p{a.dt, a.a, a.d, a.dt_bias, a.h0, a.HK, a.HV, a.softplus, 
+               static_cast<__nv_bfloat16 *>(a.y),
                reinterpret_cast<float *>(ws + cut.state), reinterpret_cast<float *>(ws + cut.decay),
                reinterpret_cast<unsigned int *>(ws), states, a.hT != nullptr,
                (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0,

@@ -2,6 +2,8 @@
 around a block (C ABI in ``include/gdn.h``; argument marshalling only)."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from .gdn import CONV_SILU, GDN_BF16, GDN_F32, GDN_OK, GDNError, load_library
@@ -71,29 +73,22 @@ def _cuda(t, name):
     return t.device
 
 
-class _On:
-    """The tensors' device as the current one, and the caller's stream as the current one
-    for what is allocated here."""
-    __slots__ = ("ctx", "raw")
+def _elsewhere(dev, stream):
+    """Whether a call has to run on another stream or device than the current ones."""
+    return stream is not None or dev.index != torch.cuda.current_device()
 
-    def __init__(self, dev, stream):
-        self.ctx = []
-        if stream is not None:
-            self.ctx.append(torch.cuda.stream(stream))
-            self.raw = stream.cuda_stream
-        else:
-            self.raw = torch.cuda.current_stream(dev).cuda_stream
-        if torch.cuda.current_device() != dev.index:
-            self.ctx.append(torch.cuda.device(dev))
 
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return self.raw
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The tensors' device and the caller's stream as the current ones, so that what is
+    allocated here belongs to the stream that uses it."""
+    with torch.cuda.device(dev):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            yield
 
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def gdn_ssm_prefill_workspace_size(N, T, HK, HV, dk, dv, dtype, varlen) -> int:
@@ -116,6 +111,10 @@ def gdn_ssm_prefill(x, b, c, dt, a, d=None, dt_bias=None, h0=None, cu_seqlens=No
     """
     lib = load_library()
     dev = _cuda(x, "x")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return gdn_ssm_prefill(x, b, c, dt, a, d, dt_bias, h0, cu_seqlens, softplus, y, hT,
+                                   workspace, None, output_final_state)
     code = _code(x, "x")
     if x.dim() != 4 or not isinstance(b, torch.Tensor) or b.dim() != 4:
         raise ValueError("expected x [B,T,HV,dv] and b, c [B,T,HK,dk]")
@@ -138,24 +137,27 @@ def gdn_ssm_prefill(x, b, c, dt, a, d=None, dt_bias=None, h0=None, cu_seqlens=No
         cu_p = _check(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
     h0_p = _opt(h0, "h0", (N, HV, dv, dk), f32, dev)
     x_row, b_row, c_row = _rows(x, "x", 2), _rows(b, "b", 2), _rows(c, "c", 2)
-    with _On(dev, stream) as raw:
-        if y is None:
-            y = torch.empty((B, T, HV, dv), dtype=x.dtype, device=dev)
-        y_p = _check(y, "y", (B, T, HV, dv), x.dtype, dev)
-        if hT is None and output_final_state:
-            hT = torch.empty((N, HV, dv, dk), dtype=f32, device=dev)
-        hT_p = _opt(hT, "hT", (N, HV, dv, dk), f32, dev)
-        if workspace is None:
-            need = lib.gdn_ssm_prefill_workspace_size(N, T, HK, HV, dk, dv, code, cu_p is not None)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_p, ws_bytes = None, 0
-        if workspace is not None:
-            ws_p = _check(workspace, "workspace", workspace.shape, workspace.dtype, dev)
-            ws_bytes = workspace.numel() * workspace.element_size()
-        st = lib.gdn_ssm_prefill(x.data_ptr(), b.data_ptr(), c.data_ptr(), dt_p, a_p, d_p, bias_p,
-                                 h0_p, cu_p, N, T, HK, HV, dk, dv, x_row, b_row, c_row,
-                                 SSM_SOFTPLUS if softplus else 0, code, y_p, hT_p, ws_p, ws_bytes, raw)
+    y_p = None if y is None else _check(y, "y", (B, T, HV, dv), x.dtype, dev)
+    if y is None:
+        y = x.new_empty((B, T, HV, dv))
+        y_p = y.data_ptr()
+    hT_p = _opt(hT, "hT", (N, HV, dv, dk), f32, dev)
+    if hT is None and output_final_state:
+        hT = dt.new_empty((N, HV, dv, dk))
+        hT_p = hT.data_ptr()
+    ws_p, ws_bytes = None, 0
+    if workspace is None:
+        ws_bytes = lib.gdn_ssm_prefill_workspace_size(N, T, HK, HV, dk, dv, code, cu_p is not None)
+        if ws_bytes:
+            workspace = dt.new_empty((ws_bytes + 3) // 4)
+            ws_p = workspace.data_ptr()
+    else:
+        ws_p = _check(workspace, "workspace", workspace.shape, workspace.dtype, dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = lib.gdn_ssm_prefill(x.data_ptr(), b.data_ptr(), c.data_ptr(), dt_p, a_p, d_p, bias_p, h0_p,
+                             cu_p, N, T, HK, HV, dk, dv, x_row, b_row, c_row,
+                             SSM_SOFTPLUS if softplus else 0, code, y_p, hT_p, ws_p, ws_bytes,
+                             _raw_stream(dev))
     if st != GDN_OK:
         raise GDNError(st, "gdn_ssm_prefill")
     return y, hT
@@ -178,6 +180,10 @@ def gdn_ssm_step(xbc, dt, a, state, d=None, dt_bias=None, conv_weight=None, conv
     """
     lib = load_library()
     dev = _cuda(xbc, "xbc")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return gdn_ssm_step(xbc, dt, a, state, d, dt_bias, conv_weight, conv_bias, conv_state,
+                                silu, softplus, state_out, conv_state_out, y, workspace)
     code = _code(xbc, "xbc")
     if xbc.dim() != 2 or not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("expected xbc [N, HV*dv + 2*HK*dk] and state [N,HV,dv,dk]")
@@ -206,18 +212,21 @@ def gdn_ssm_step(xbc, dt, a, state, d=None, dt_bias=None, conv_weight=None, conv
         if conv_state_out is not None:
             co_p = _check(conv_state_out, "conv_state_out", (N, W - 1, C), xbc.dtype, dev)
     row = _rows(xbc, "xbc", 1)
-    with _On(dev, stream) as raw:
-        if y is None:
-            y = torch.empty((N, HV, dv), dtype=xbc.dtype, device=dev)
-        y_p = _check(y, "y", (N, HV, dv), xbc.dtype, dev)
-        if workspace is None:
-            workspace = torch.empty(lib.gdn_ssm_step_workspace_size(N, HK, HV, dk, dv),
-                                    dtype=torch.uint8, device=dev)
+    y_p = None if y is None else _check(y, "y", (N, HV, dv), xbc.dtype, dev)
+    if y is None:
+        y = xbc.new_empty((N, HV, dv))
+        y_p = y.data_ptr()
+    if workspace is None:
+        ws_bytes = lib.gdn_ssm_step_workspace_size(N, HK, HV, dk, dv)
+        workspace = dt.new_empty((ws_bytes + 3) // 4)
+        ws_p = workspace.data_ptr()
+    else:
         ws_p = _check(workspace, "workspace", workspace.shape, workspace.dtype, dev)
-        st = lib.gdn_ssm_step(xbc.data_ptr(), dt_p, a_p, d_p, bias_p, w_p, cb_p, cs_p, co_p, W,
-                              state_p, out_p, N, HK, HV, dk, dv, row,
-                              (SSM_SOFTPLUS if softplus else 0) | (CONV_SILU if silu else 0), code,
-                              y_p, ws_p, workspace.numel() * workspace.element_size(), raw)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = lib.gdn_ssm_step(xbc.data_ptr(), dt_p, a_p, d_p, bias_p, w_p, cb_p, cs_p, co_p, W, state_p,
+                          out_p, N, HK, HV, dk, dv, row,
+                          (SSM_SOFTPLUS if softplus else 0) | (CONV_SILU if silu else 0), code, y_p,
+                          ws_p, ws_bytes, _raw_stream(dev))
     if st != GDN_OK:
         raise GDNError(st, "gdn_ssm_step")
     return y
@@ -242,6 +251,9 @@ def gdn_gated_norm(o, z=None, weight=None, eps: float = 1e-6, gate: str = "sigmo
     """
     lib = load_library()
     dev = _cuda(o, "o")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return gdn_gated_norm(o, z, weight, eps, gate, gate_first, unit_offset, y)
     code = _code(o, "o")
     if o.dim() < 2:
         raise ValueError("expected o [..., G, D]")
@@ -257,14 +269,15 @@ def gdn_gated_norm(o, z=None, weight=None, eps: float = 1e-6, gate: str = "sigmo
             wg = G
         w_p = _check(weight, "weight", (G, D) if weight.dim() == 2 else (D,), torch.float32, dev)
     o_row = _rows(o, "o", 2)
-    with _On(dev, stream) as raw:
-        if y is None:
-            y = torch.empty(o.shape, dtype=o.dtype, device=dev)
-        y_p = _check(y, "y", o.shape, o.dtype, dev)
-        if o.numel() == 0:
-            return y
-        st = lib.gdn_gated_norm(o.data_ptr(), z_p, w_p, o.numel() // (G * D), G, D, o_row, z_row, wg,
-                                eps, flags, code, y_p, raw)
+    y_p = None if y is None else _check(y, "y", o.shape, o.dtype, dev)
+    if y is None:
+        y = o.new_empty(o.shape)
+        y_p = y.data_ptr()
+    n = o.numel()
+    if n == 0:
+        return y
+    st = lib.gdn_gated_norm(o.data_ptr(), z_p, w_p, n // (G * D), G, D, o_row, z_row, wg, eps, flags,
+                            code, y_p, _raw_stream(dev))
     if st != GDN_OK:
         raise GDNError(st, "gdn_gated_norm")
     return y
@@ -283,6 +296,10 @@ def gdn_residual_norm(x, residual=None, weight=None, post_weight=None, z=None, s
     """
     lib = load_library()
     dev = _cuda(x, "x")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return gdn_residual_norm(x, residual, weight, post_weight, z, scale, eps, gate,
+                                     unit_offset, residual_out, y)
     code = _code(x, "x")
     if x.dim() < 1:
         raise ValueError("expected x [..., C]")
@@ -298,17 +315,19 @@ def gdn_residual_norm(x, residual=None, weight=None, post_weight=None, z=None, s
     z_p = _opt(z, "z", shape, x.dtype, dev)
     w_p = _opt(weight, "weight", (C,), f32, dev)
     pw_p = _opt(post_weight, "post_weight", (C,), f32, dev)
-    with _On(dev, stream) as raw:
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=rdtype, device=dev)
-        ro_p = _check(residual_out, "residual_out", shape, rdtype, dev)
-        if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=dev)
-        y_p = _check(y, "y", shape, x.dtype, dev)
-        if x.numel() == 0:
-            return y, residual_out
-        st = lib.gdn_residual_norm(x_p, r_p, w_p, pw_p, z_p, x.numel() // C, C, scale, eps, flags,
-                                   code, _CODES[rdtype], ro_p, y_p, raw)
+    ro_p = _opt(residual_out, "residual_out", shape, rdtype, dev)
+    if residual_out is None:
+        residual_out = kept.new_empty(shape)
+        ro_p = residual_out.data_ptr()
+    y_p = None if y is None else _check(y, "y", shape, x.dtype, dev)
+    if y is None:
+        y = x.new_empty(shape)
+        y_p = y.data_ptr()
+    n = x.numel()
+    if n == 0:
+        return y, residual_out
+    st = lib.gdn_residual_norm(x_p, r_p, w_p, pw_p, z_p, n // C, C, scale, eps, flags, code,
+                               _CODES[rdtype], ro_p, y_p, _raw_stream(dev))
     if st != GDN_OK:
         raise GDNError(st, "gdn_residual_norm")
     return y, residual_out
