@@ -167,13 +167,6 @@ __device__ __forceinline__ float2 subp(float2 a, float2 b) {
     memcpy(&d, &ud, 8);
     return d;
 }
-// x -> bf16 pair word, and the exact remainder
-__device__ __forceinline__ uint32_t take_bf16(float2 &x) {
-    const uint32_t w = pack_bf16x2(x.x, x.y);
-    x = subp(x, unpack2(w));
-    return w;
-}
-
 // One head's decay and step bias, a * log2 e and dt_bias.
 struct HeadTab {
     float ah, bias;
@@ -218,13 +211,14 @@ struct StatesCfg {
     static constexpr uint32_t XT = VT * 256;                 // x tile: 128 rows
     static constexpr uint32_t STAGE = 32768 + XT;            // b tile, x tile
     static constexpr int NS = 3;
-    static constexpr uint32_t O_TAB = NS * STAGE;            // w to the chunk's end [2][NH][128]
-    static constexpr uint32_t O_BAR = O_TAB + 2 * NH * 512;
+    static constexpr uint32_t O_TAB = NS * STAGE;            // w to the 32-token block's end [NS][NH][128]
+    static constexpr uint32_t O_SUM = O_TAB + NS * NH * 512; // the blocks' log2 decays [NS][NH][4]
+    static constexpr uint32_t O_BAR = O_SUM + NS * NH * 16;
     static constexpr uint32_t BYTES = O_BAR + 256 + 1024;
 };
 static_assert(StatesCfg<128, 2>::BYTES <= 232448, "shared memory");
-constexpr int kStWorkers = 16, kStWork0 = 4, kStThreads = (kStWork0 + kStWorkers) * 32;
-enum StBar { SB_F0, SB_E0 = SB_F0 + 3, SB_TF0 = SB_E0 + 3, SB_TF1, SB_TE0, SB_TE1, SB_WF0, SB_WF1, SB_WE0, SB_WE1,
+constexpr int kStTables = 4, kStTable0 = 2, kStWorkers = 16, kStWork0 = kStTable0 + kStTables, kStThreads = (kStWork0 + kStWorkers) * 32;
+enum StBar { SB_F0, SB_E0 = SB_F0 + 3, SB_TF0 = SB_E0 + 3, SB_TE0 = SB_TF0 + 3, SB_WF0 = SB_TE0 + 3, SB_WF1, SB_WE0, SB_WE1,
              SB_DONE, SB_READ, SB_END, SB_COUNT };
 constexpr int kFlush = 8;   // chunks between two readings of the accumulators
 // tensor memory: the sums of the first terms, of the small ones, two pieces of 64 tokens
@@ -268,7 +262,6 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::O_BAR);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cfg::O_BAR + 8 * SB_COUNT);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cfg::O_BAR + 8 * SB_COUNT + 4);
-    float *sums = reinterpret_cast<float *>(sm + Cfg::O_BAR + 8 * SB_COUNT + 8);   // log2 decays of a chunk [2][NH]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.HV / NH;
     const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
@@ -279,10 +272,10 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bars[SB_F0 + i], 1);
             mbar_init(&bars[SB_E0 + i], 1 + kStWorkers);
+            mbar_init(&bars[SB_TF0 + i], kStTables);
+            mbar_init(&bars[SB_TE0 + i], kStWorkers);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[SB_TF0 + i], 1);
-            mbar_init(&bars[SB_TE0 + i], kStWorkers);
             mbar_init(&bars[SB_WF0 + i], kStWorkers);
             mbar_init(&bars[SB_WE0 + i], 1);
         }
@@ -292,7 +285,7 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 3) tmem_alloc(tslot, 512);
+    if (warp == 2) tmem_alloc(tslot, 512);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
@@ -359,48 +352,38 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         if (elect_one()) mma_commit(&bars[SB_END]);
         __syncwarp();
         wt.drain(SB_END, 0);
-    } else if (warp == 2 || warp == 3) {
-        // the weights to the chunk's end, every other chunk each
+    } else if (warp < kStWork0) {
+        // a 32-token block of every chunk each: the weights to the block's end, and its decay
+        const int q = warp - kStTable0;
         HeadTab ht[NH];
 #pragma unroll
         for (int e = 0; e < NH; ++e) ht[e] = {p.a[head + e] * kLog2e, p.dt_bias ? p.dt_bias[head + e] : 0.f};
         const float *dtp = p.dt + seg.t0 * p.HV + head;
-        auto load_dt = [&](int j, int q, int e) {
+        auto load_dt = [&](int j, int e) {
             const int t = chunk_of(j) * L + 32 * q + lane;
             return t >= 0 && t < seg.len ? __ldg(dtp + (int64_t)t * p.HV + e) : 0.f;
         };
-        // four blocks of dt on their way, the one used next last
-        const int first = warp - 2;
-        float ahead[NH][4];
+        float ahead[NH][2];     // dt of the next two chunks
 #pragma unroll
-        for (int e = 0; e < NH; ++e)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ahead[e][q] = load_dt(first, q, e);
-        for (int j = first; j < nch && ok; j += 2) {
-            const int s = j & 1;
-            if (j >= 2) ok = wt(SB_TE0 + s, (uint32_t)(((j >> 1) - 1) & 1));
-            if (!ok) break;
-            float *tab = reinterpret_cast<float *>(sm + Cfg::O_TAB + s * NH * 512);
-            float behind[NH];
-#pragma unroll
-            for (int e = 0; e < NH; ++e) behind[e] = 0.f;
+        for (int e = 0; e < NH; ++e) {
+            ahead[e][0] = load_dt(0, e);
+            ahead[e][1] = load_dt(1, e);
+        }
 #pragma unroll 1
-            for (int q = 3; q >= 0; --q) {
-                const bool in = chunk_of(j) * L + 32 * q + lane < seg.len;
+        for (int j = 0; j < nch; ++j) {
+            const int s = j % 3;
+            if (j >= 3 && !wt(SB_TE0 + s, (uint32_t)((j / 3 - 1) & 1))) break;
+            const bool in = chunk_of(j) * L + 32 * q + lane < seg.len;
 #pragma unroll
-                for (int e = 0; e < NH; ++e) {
-                    float delta, g, pre, suf;
-                    token_step(ahead[e][3], ht[e], in, p.soft, delta, g);
-                    ahead[e][3] = ahead[e][2];
-                    ahead[e][2] = ahead[e][1];
-                    ahead[e][1] = ahead[e][0];
-                    ahead[e][0] = load_dt(j + 2, q, e);
-                    const float sum = block_sums(g, lane, pre, suf);
-                    tab[e * 128 + 32 * q + lane] = delta * ex2(suf + behind[e]);
-                    behind[e] += sum;
-                }
+            for (int e = 0; e < NH; ++e) {
+                float delta, g, pre, suf;
+                token_step(ahead[e][0], ht[e], in, p.soft, delta, g);
+                ahead[e][0] = ahead[e][1];
+                ahead[e][1] = load_dt(j + 2, e);
+                const float sum = block_sums(g, lane, pre, suf);
+                reinterpret_cast<float *>(sm + Cfg::O_TAB + (s * NH + e) * 512)[32 * q + lane] = delta * ex2(suf);
+                if (lane == 0) reinterpret_cast<float *>(sm + Cfg::O_SUM + (s * NH + e) * 16)[q] = sum;
             }
-            if (lane < NH) sums[s * NH + lane] = NH == 2 && lane == 1 ? behind[NH - 1] : behind[0];
             warp_arrive(&bars[SB_TF0 + s]);
         }
     } else if (warp >= kStWork0) {
@@ -411,26 +394,26 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         const int e = NH == 2 ? quad >> 1 : 0;
         // this lane's row of the 8x8 blocks: token (lane & 7) + 8 of blocks 2, 3; columns + 8 of blocks 1, 3
         const int trow = 16 * th + (lane & 7) + 8 * (lane >> 4), vblk = (lane >> 3) & 1;
-        float run[NH], acc[32];      // log2 decays behind the chunk; the sums
-#pragma unroll
-        for (int h = 0; h < NH; ++h) run[h] = 0.f;
+        float run = 0.f, acc[32];      // log2 decays behind the chunk; the sums
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[i] = 0.f;
         for (int j = 0; j < nch && ok; ++j) {
-            const int s = j & 1, len = len_of(j);
-            ok = stage_full(j) && wt(SB_TF0 + s, (uint32_t)((j >> 1) & 1));
+            const int s = j % 3, len = len_of(j);
+            ok = stage_full(j) && wt(SB_TF0 + s, (uint32_t)((j / 3) & 1));
             if (!ok) break;
-            const uint32_t stage = sb + (j % 3) * Cfg::STAGE;
+            const uint32_t stage = sb + s * Cfg::STAGE;
             const float *tab = reinterpret_cast<const float *>(sm + Cfg::O_TAB + (s * NH + e) * 512);
-            const float far = ex2(NH == 2 && e == 1 ? run[NH - 1] : run[0]);
-#pragma unroll
-            for (int h = 0; h < NH; ++h) run[h] += sums[s * NH + h];
+            const float4 sum = *reinterpret_cast<const float4 *>(sm + Cfg::O_SUM + (s * NH + e) * 16);
+            // decays behind this thread's blocks (tokens 16 th of either half of the chunk)
+            const float after1 = th < 2 ? sum.w + run : run, after0 = th < 2 ? (sum.y + sum.z) + (sum.w + run) : sum.z + (sum.w + run);
+            run += (sum.x + sum.y) + (sum.z + sum.w);
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 const int pc = 2 * j + q, r = pc & 1;
                 if (pc >= 2) ok = wt(SB_WE0 + r, (uint32_t)(((pc >> 1) - 1) & 1));
                 if (!ok) break;
                 if (mine) {
+                    const float far = ex2(q ? after1 : after0);
                     const int tok = 64 * q + 16 * th + 2 * (lane & 3);   // + 8 i + {0, 1}
                     float2 w2[2];
 #pragma unroll
@@ -477,7 +460,7 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                 warp_arrive(&bars[SB_WF0 + r]);
             }
             if (!ok) break;
-            warp_arrive(&bars[SB_E0 + j % 3]);
+            warp_arrive(&bars[SB_E0 + s]);
             warp_arrive(&bars[SB_TE0 + s]);
             if (j % kFlush == kFlush - 1 || j == nch - 1) {
                 ok = wt(SB_DONE, (uint32_t)((j / kFlush) & 1));
@@ -496,7 +479,9 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                 warp_arrive(&bars[SB_READ]);
             }
         }
-        if (ok && tid < NH) p.seg_decay[(size_t)slot * p.HV + head + tid] = ex2(NH == 2 && tid == 1 ? run[NH - 1] : run[0]);
+        // (quadrant 0 has the first head, quadrant 2 the second)
+        if (ok && th == 0 && lane == 0 && (quad == 0 || (NH == 2 && quad == 2)))
+            p.seg_decay[(size_t)slot * p.HV + head + e] = ex2(run);
         if (ok && mine) {
             const int v = 32 * quad + lane, h = head + v / DV;
             float4 *dst = reinterpret_cast<float4 *>(p.seg_state + (((size_t)slot * p.HV + h) * DV + v % DV) * DK + 32 * th);
@@ -505,7 +490,7 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         }
     }
     __syncthreads();
-    if (warp == 3) {
+    if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
