@@ -218,12 +218,13 @@ struct StatesCfg {
 };
 static_assert(StatesCfg<128, 2>::BYTES <= 232448, "shared memory");
 constexpr int kStTables = 4, kStTable0 = 2, kStWorkers = 16, kStWork0 = kStTable0 + kStTables, kStThreads = (kStWork0 + kStWorkers) * 32;
-enum StBar { SB_F0, SB_E0 = SB_F0 + 3, SB_TF0 = SB_E0 + 3, SB_TE0 = SB_TF0 + 3, SB_WF0 = SB_TE0 + 3, SB_WF1, SB_WE0, SB_WE1,
-             SB_DONE, SB_READ, SB_END, SB_COUNT };
+enum StBar { SB_F0, SB_E0 = SB_F0 + 3, SB_TF0 = SB_E0 + 3, SB_TE0 = SB_TF0 + 3, SB_WF0 = SB_TE0 + 3, SB_WE0 = SB_WF0 + 5,
+             SB_DONE = SB_WE0 + 5, SB_READ, SB_END, SB_COUNT };
 constexpr int kFlush = 8;   // chunks between two readings of the accumulators
-// tensor memory: the sums of the first terms, of the small ones, two pieces of 64 tokens
-// (three terms of 32 columns)
-constexpr uint32_t TS_D = 0, TS_DS = 128, TS_A = 256, TS_PIECE = 96;
+// tensor memory: the sums of the first terms, of the small ones, a ring of pieces of 32
+// tokens (three terms of 16 columns)
+constexpr uint32_t TS_D = 0, TS_DS = 128, TS_A = 256, TS_PIECE = 48;
+constexpr int kPieces = 5;
 
 // four 8x8 blocks of 16-bit elements, each transposed over the warp; lane l gives the
 // address of row l % 8 of block l / 8
@@ -232,11 +233,11 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-// 16 lanes x 8 columns: registers 2i, 2i + 1 hold columns 4i .. 4i + 3 of lanes l / 4 and
+// 16 lanes x 16 columns: registers 2i, 2i + 1 hold columns 4i .. 4i + 3 of lanes l / 4 and
 // l / 4 + 8 (column l % 4 of the four)
-__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&w)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3])
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&w)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
 // The upper halves of two floats as a bf16 pair (truncated), the floats' remainders left:
@@ -275,8 +276,8 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             mbar_init(&bars[SB_TF0 + i], kStTables);
             mbar_init(&bars[SB_TE0 + i], kStWorkers);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[SB_WF0 + i], kStWorkers);
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&bars[SB_WF0 + i], 4);
             mbar_init(&bars[SB_WE0 + i], 1);
         }
         mbar_init(&bars[SB_DONE], 1);
@@ -326,24 +327,26 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             ok = ok && stage_full(j);
             const uint64_t b0 = sdesc_sw128(sb + (j % 3) * Cfg::STAGE, 16384, 1024);
 #pragma unroll 1
-            for (int q = 0; q < 2 && ok; ++q) {
-                const int pc = 2 * j + q, r = pc & 1;
-                ok = wt(SB_WF0 + r, (uint32_t)((pc >> 1) & 1));
+            for (int q = 0; q < 4 && ok; ++q) {
+                const int pc = 4 * j + q, r = pc % kPieces;
+                ok = wt(SB_WF0 + r, (uint32_t)((pc / kPieces) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t bd = desc_add(b0, q * 8192 + k * 2048);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint64_t bd = desc_add(b0, q * 4096 + k * 2048);
                         const uint32_t a = tmem + TS_A + r * TS_PIECE + 8 * k;
                         const uint32_t add = !fresh || q + k > 0;
                         mma_bf16_ts(tmem + TS_D, a, bd, id, add);
-                        mma_bf16_ts(tmem + TS_DS, a + 32, bd, id, add);
-                        mma_bf16_ts(tmem + TS_DS, a + 64, bd, id, 1);
+                        mma_bf16_ts(tmem + TS_DS, a + 16, bd, id, add);
+                        mma_bf16_ts(tmem + TS_DS, a + 32, bd, id, 1);
                     }
                     mma_commit(&bars[SB_WE0 + r]);
-                    if (q == 1) mma_commit(&bars[SB_E0 + j % 3]);
-                    if (q == 1 && (j % kFlush == kFlush - 1 || j == nch - 1)) mma_commit(&bars[SB_DONE]);
+                    if (q == 3) {
+                        mma_commit(&bars[SB_E0 + j % 3]);
+                        if (j % kFlush == kFlush - 1 || j == nch - 1) mma_commit(&bars[SB_DONE]);
+                    }
                 }
                 __syncwarp();
             }
@@ -387,13 +390,14 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             warp_arrive(&bars[SB_TF0 + s]);
         }
     } else if (warp >= kStWork0) {
-        // lanes (value columns) 32 quad .. + 31; tokens 16 th .. + 15 of every piece, and
-        // columns 32 th .. + 31 of the sums
-        const int quad = warp & 3, th = (warp - kStWork0) >> 2, tid = threadIdx.x - kStWork0 * 32;
+        // lanes (value columns) 32 quad .. + 31; block th of every chunk is a piece, formed by
+        // four warps; and columns 32 th .. + 31 of the sums
+        const int quad = warp & 3, th = (warp - kStWork0) >> 2;
         const bool mine = 32 * quad < VT;                       // (a tile of 64 fills half of the lanes)
         const int e = NH == 2 ? quad >> 1 : 0;
         // this lane's row of the 8x8 blocks: token (lane & 7) + 8 of blocks 2, 3; columns + 8 of blocks 1, 3
-        const int trow = 16 * th + (lane & 7) + 8 * (lane >> 4), vblk = (lane >> 3) & 1;
+        const int trow = 32 * th + (lane & 7) + 8 * (lane >> 4), vblk = (lane >> 3) & 1;
+        const int tok = 32 * th + 2 * (lane & 3);               // this lane's tokens: + 8 b + {0, 1}
         float run = 0.f, acc[32];      // log2 decays behind the chunk; the sums
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[i] = 0.f;
@@ -404,62 +408,60 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             const uint32_t stage = sb + s * Cfg::STAGE;
             const float *tab = reinterpret_cast<const float *>(sm + Cfg::O_TAB + (s * NH + e) * 512);
             const float4 sum = *reinterpret_cast<const float4 *>(sm + Cfg::O_SUM + (s * NH + e) * 16);
-            // decays behind this thread's blocks (tokens 16 th of either half of the chunk)
-            const float after1 = th < 2 ? sum.w + run : run, after0 = th < 2 ? (sum.y + sum.z) + (sum.w + run) : sum.z + (sum.w + run);
+            float after = run;         // ... and behind this block
+            if (th < 3) after += sum.w;
+            if (th < 2) after += sum.z;
+            if (th < 1) after += sum.y;
             run += (sum.x + sum.y) + (sum.z + sum.w);
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-                const int pc = 2 * j + q, r = pc & 1;
-                if (pc >= 2) ok = wt(SB_WE0 + r, (uint32_t)(((pc >> 1) - 1) & 1));
-                if (!ok) break;
-                if (mine) {
-                    const float far = ex2(q ? after1 : after0);
-                    const int tok = 64 * q + 16 * th + 2 * (lane & 3);   // + 8 i + {0, 1}
-                    float2 w2[2];
+            const float far = ex2(after);
+            float2 w2[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        w2[i] = *reinterpret_cast<const float2 *>(tab + tok + 8 * i);
-                        w2[i] = mulp(w2[i], make_float2(far, far));
-                    }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const int col = 32 * quad + 16 * g + 8 * vblk;
-                        uint32_t x[4], hi[4], mid[4], lo[4];
-                        ldsm_x4_t(stage + 32768 + (col >> 6) * 16384 + sw128_chunk(64 * q + trow, (col & 63) >> 3), x);
-                        if (len < L) {   // rows behind the sequence may hold anything
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int t = tok + 8 * (i >> 1);
-                                if (t >= len) x[i] = 0u;
-                                if (t + 1 >= len) x[i] &= 0xffffu;
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float2 f = mulp(unpack2(x[i]), w2[i >> 1]);
-                            hi[i] = take_high(f);
-                            mid[i] = take_high(f);
-                            lo[i] = high_pair(f);
-                        }
-                        const uint32_t ta = tmem + ((uint32_t)(32 * quad + 16 * g) << 16) + TS_A + r * TS_PIECE + 8 * th;
-                        tmem_st_16x128b_x2(ta, hi);
-                        tmem_st_16x128b_x2(ta + 32, mid);
-                        tmem_st_16x128b_x2(ta + 64, lo);
-                    }
-                    tmem_wait_st();
-                }
-                if (len < L) {
-                    // rows of b behind the sequence: a NaN there must not meet the zeros
-                    for (int v = tid; v < 64 * 16; v += kStWorkers * 32) {
-                        const int row = 64 * q + (v >> 4), ch = v & 15;
-                        if (row >= len) sts128(stage + (ch >> 3) * 16384 + row * 128 + (ch & 7) * 16, 0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tc_fence_before();
-                warp_arrive(&bars[SB_WF0 + r]);
-            }
+            for (int b = 0; b < 4; ++b)
+                w2[b] = mulp(*reinterpret_cast<const float2 *>(tab + tok + 8 * b), make_float2(far, far));
+            const int pc = 4 * j + th, r = pc % kPieces;
+            if (pc >= kPieces) ok = wt(SB_WE0 + r, (uint32_t)((pc / kPieces - 1) & 1));
             if (!ok) break;
+            if (mine) {
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    const int col = 32 * quad + 16 * g + 8 * vblk;
+                    const uint32_t base = stage + 32768 + (col >> 6) * 16384;
+                    uint32_t x[2][4], hi[8], mid[8], lo[8];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) ldsm_x4_t(base + sw128_chunk(trow + 16 * b, (col & 63) >> 3), x[b]);
+                    if (len < L) {   // rows behind the sequence may hold anything
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int t = tok + 8 * (i >> 1);
+                            if (t >= len) x[i >> 2][i & 3] = 0u;
+                            if (t + 1 >= len) x[i >> 2][i & 3] &= 0xffffu;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float2 f = mulp(unpack2(x[i >> 2][i & 3]), w2[i >> 1]);
+                        hi[i] = take_high(f);
+                        mid[i] = take_high(f);
+                        lo[i] = high_pair(f);
+                    }
+                    const uint32_t ta = tmem + ((uint32_t)(32 * quad + 16 * g) << 16) + TS_A + r * TS_PIECE;
+                    tmem_st_16x128b_x4(ta, hi);
+                    tmem_st_16x128b_x4(ta + 16, mid);
+                    tmem_st_16x128b_x4(ta + 32, lo);
+                }
+                tmem_wait_st();
+            }
+            if (len < L) {
+                // rows of b behind the sequence: a NaN there must not meet the zeros (each block's
+                // by its four warps)
+                for (int v = 32 * quad + lane; v < 32 * 16; v += 128) {
+                    const int row = 32 * th + (v >> 4), ch = v & 15;
+                    if (row >= len) sts128(stage + (ch >> 3) * 16384 + row * 128 + (ch & 7) * 16, 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            warp_arrive(&bars[SB_WF0 + r]);
             warp_arrive(&bars[SB_E0 + s]);
             warp_arrive(&bars[SB_TE0 + s]);
             if (j % kFlush == kFlush - 1 || j == nch - 1) {
