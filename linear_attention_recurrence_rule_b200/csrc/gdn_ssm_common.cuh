@@ -58,6 +58,27 @@ bool tc_supported(const SsmArgs &a);
 size_t tc_workspace_bytes(const SsmArgs &a);
 cudaError_t launch_tc(const SsmArgs &a, cudaStream_t stream);
 
+// Dependent launches: a kernel launched with launch_after may start while the one
+// before it in the stream still runs; wait_for_previous() returns when that one is done
+// (and with it all before it), let_next_start() lets the next one start early.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+    return err == cudaSuccess ? cudaGetLastError() : err;
+}
+
 // log(1 + e^x), finite and accurate at both ends
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 

@@ -19,7 +19,9 @@
 namespace gdn {
 namespace {
 
+using ssm::let_next_start;
 using ssm::step_size;
+using ssm::wait_for_previous;
 
 constexpr int kWarps = 8;
 constexpr int kRowSeqs = 4;      // sequences per thread of step_row_kernel
@@ -33,14 +35,11 @@ struct RowCall {
     bool silu, soft;
 };
 
-__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // W 0: no convolution.  grid.x: blocks of 256 channels, then the heads' gates
 template <typename T, int W>
 __global__ void __launch_bounds__(256)
 step_row_kernel(const T *__restrict__ xbc, const T *cs, T *cs_out, const RowCall p) {
-    let_dependents_start();
+    let_next_start();
     const int cblocks = (p.C + 255) / 256;
     const int n0 = blockIdx.y * kRowSeqs;
     if ((int)blockIdx.x >= cblocks) {
@@ -200,18 +199,9 @@ cudaError_t launch_dk(const SsmStepArgs &a, cudaStream_t stream) {
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     constexpr int BAND = kWarps * (32 / (DK / 4)) * 8;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.N * a.HV), (unsigned)((a.dv + BAND - 1) / BAND));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const dim3 grid((unsigned)(a.N * a.HV), (unsigned)((a.dv + BAND - 1) / BAND));
     const StepCall s{row, gates, a.d, a.state, a.state_out, a.HK, a.HV, a.dv, (size_t)C};
-    err = cudaLaunchKernelEx(&cfg, ssm_step_kernel<DK, T>, s, static_cast<T *>(a.y));
-    return err == cudaSuccess ? cudaGetLastError() : err;
+    return ssm::launch_after(ssm_step_kernel<DK, T>, grid, dim3(kWarps * 32), 0, stream, s, static_cast<T *>(a.y));
 }
 
 template <typename T>

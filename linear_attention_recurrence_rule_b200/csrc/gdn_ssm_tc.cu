@@ -266,6 +266,9 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.HV / NH;
     const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
+    let_next_start();
+    // (no wait gives up within the first second)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
     const Seg seg = find_seg(p.map, slot);
     if (!seg.ok || (seg.last && !p.whole)) return;
     const int nch = (seg.len + L - 1) / L;
@@ -544,6 +547,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.HV / NH;
     const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && !p.chained) *p.status = 0u;
     const Seg seg = find_seg(p.map, slot);
     if (!seg.ok || seg.len <= 0) return;
     const int nch = (seg.len + L - 1) / L, last = nch - 1;
@@ -835,6 +839,8 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
     } else if (warp >= kScState && warp < kScWeight) {
         // ------------------------------------------------ state (lanes k)
         const int k = 32 * (warp - kScState) + lane;
+        // the start states are the only thing here that the kernels before this one make
+        if (p.chained) wait_for_previous();
         const float *src = p.chained ? p.seg_state + ((size_t)slot * p.HV + head) * DV * DK
                            : p.h0    ? p.h0 + ((size_t)seg.n * p.HV + head) * DV * DK
                                      : nullptr;
@@ -1054,10 +1060,11 @@ cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
     if (grid > 0x7fffffff || (int64_t)a.N * a.HV > 0x7fffffff) return cudaErrorInvalidValue;
     const bool packed = a.cu_seqlens != nullptr;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    cudaError_t err = cudaMemsetAsync(ws, 0, sizeof(unsigned int), stream);
-    if (err != cudaSuccess) return err;
     const bool cuts = packed ? a.T > cut.seg_len : cut.nseg > 1;
     const bool states = cuts || a.hT != nullptr;
+    // the first kernel clears the status word; with no tokens and no states to return there is none
+    if (!states && a.T == 0) return cudaMemsetAsync(ws, 0, sizeof(unsigned int), stream);
+    cudaError_t err = cudaSuccess;
     TcParams p{a.dt, a.a, a.d, a.dt_bias, a.h0, a.HK, a.HV, a.softplus, 
                static_cast<__nv_bfloat16 *>(a.y),
                reinterpret_cast<float *>(ws + cut.state), reinterpret_cast<float *>(ws + cut.decay),
@@ -1093,6 +1100,8 @@ cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
         constexpr uint32_t bytes = ScanCfg<VT, NH>::BYTES;
         err = cudaFuncSetAttribute(scan_kernel<VT, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (err != cudaSuccess) return err;
+        if (states)
+            return launch_after(scan_kernel<VT, NH>, dim3((unsigned)grid), dim3(kScThreads), bytes, stream, tx, tb, tcm, p);
         scan_kernel<VT, NH><<<(unsigned)grid, kScThreads, bytes, stream>>>(tx, tb, tcm, p);
     }
     return cudaGetLastError();
