@@ -33,7 +33,8 @@
 // tokens through a ring of 3) and output
 // (two groups, half of the columns each).  The mask takes e^{G_i-G_j} as the decays
 // behind j in its 32-token block times those from there to i, both <= 1: one
-// exponential per row and block; only the diagonal blocks take one per element.  All
+// exponential per row and block (the diagonal blocks one per element where their decays
+// are too strong for a common reference).  All
 // sums of log decays run over the tokens between the two ends (block sums), none is a
 // difference of running sums: a token that forgets everything (a log decay of
 // thousands) would leave such differences few digits for the tokens behind it.
@@ -138,6 +139,14 @@ __device__ __forceinline__ void tmem_ld32r(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 u;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr));
@@ -233,11 +242,11 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-// 16 lanes x 16 columns: registers 2i, 2i + 1 hold columns 4i .. 4i + 3 of lanes l / 4 and
+// 16 lanes x 8 columns: registers 2i, 2i + 1 hold columns 4i .. 4i + 3 of lanes l / 4 and
 // l / 4 + 8 (column l % 4 of the four)
-__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&w)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&w)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
                  : "memory");
 }
 // The upper halves of two floats as a bf16 pair (truncated), the floats' remainders left:
@@ -417,40 +426,41 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             if (th < 1) after += sum.y;
             run += (sum.x + sum.y) + (sum.z + sum.w);
             const float far = ex2(after);
-            float2 w2[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                w2[b] = mulp(*reinterpret_cast<const float2 *>(tab + tok + 8 * b), make_float2(far, far));
             const int pc = 4 * j + th, r = pc % kPieces;
             if (pc >= kPieces) ok = wt(SB_WE0 + r, (uint32_t)((pc / kPieces - 1) & 1));
             if (!ok) break;
             if (mine) {
 #pragma unroll 1
-                for (int g = 0; g < 2; ++g) {
-                    const int col = 32 * quad + 16 * g + 8 * vblk;
-                    const uint32_t base = stage + 32768 + (col >> 6) * 16384;
-                    uint32_t x[2][4], hi[8], mid[8], lo[8];
+                for (int b = 0; b < 2; ++b) {
+                    float2 w2[2];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) ldsm_x4_t(base + sw128_chunk(trow + 16 * b, (col & 63) >> 3), x[b]);
-                    if (len < L) {   // rows behind the sequence may hold anything
+                    for (int i = 0; i < 2; ++i)
+                        w2[i] = mulp(*reinterpret_cast<const float2 *>(tab + tok + 16 * b + 8 * i), make_float2(far, far));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int t = tok + 8 * (i >> 1);
-                            if (t >= len) x[i >> 2][i & 3] = 0u;
-                            if (t + 1 >= len) x[i >> 2][i & 3] &= 0xffffu;
+                    for (int g = 0; g < 2; ++g) {
+                        const int col = 32 * quad + 16 * g + 8 * vblk;
+                        uint32_t x[4], hi[4], mid[4], lo[4];
+                        ldsm_x4_t(stage + 32768 + (col >> 6) * 16384 + sw128_chunk(trow + 16 * b, (col & 63) >> 3), x);
+                        if (len < L) {   // rows behind the sequence may hold anything
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int t = tok + 16 * b + 8 * (i >> 1);
+                                if (t >= len) x[i] = 0u;
+                                if (t + 1 >= len) x[i] &= 0xffffu;
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 f = mulp(unpack2(x[i >> 2][i & 3]), w2[i >> 1]);
-                        hi[i] = take_high(f);
-                        mid[i] = take_high(f);
-                        lo[i] = high_pair(f);
+                        for (int i = 0; i < 4; ++i) {
+                            float2 f = mulp(unpack2(x[i]), w2[i >> 1]);
+                            hi[i] = take_high(f);
+                            mid[i] = take_high(f);
+                            lo[i] = high_pair(f);
+                        }
+                        const uint32_t ta = tmem + ((uint32_t)(32 * quad + 16 * g) << 16) + TS_A + r * TS_PIECE + 8 * b;
+                        tmem_st_16x128b_x2(ta, hi);
+                        tmem_st_16x128b_x2(ta + 16, mid);
+                        tmem_st_16x128b_x2(ta + 32, lo);
                     }
-                    const uint32_t ta = tmem + ((uint32_t)(32 * quad + 16 * g) << 16) + TS_A + r * TS_PIECE;
-                    tmem_st_16x128b_x4(ta, hi);
-                    tmem_st_16x128b_x4(ta + 16, mid);
-                    tmem_st_16x128b_x4(ta + 32, lo);
                 }
                 tmem_wait_st();
             }
@@ -472,27 +482,28 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float hi[16], small[16];
-                    tmem_ld16(tmem_addr(tmem, warp, TS_D + 32 * th + 16 * g), hi);
-                    tmem_ld16(tmem_addr(tmem, warp, TS_DS + 32 * th + 16 * g), small);
+                for (int g = 0; g < 4; ++g) {
+                    float hi[8], small[8];
+                    tmem_ld8(tmem_addr(tmem, warp, TS_D + 32 * th + 8 * g), hi);
+                    tmem_ld8(tmem_addr(tmem, warp, TS_DS + 32 * th + 8 * g), small);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[16 * g + i] += hi[i] + small[i];
+                    for (int i = 0; i < 8; ++i) acc[8 * g + i] += hi[i] + small[i];
                 }
                 tc_fence_before();
                 warp_arrive(&bars[SB_READ]);
             }
         }
-        // (quadrant 0 has the first head, quadrant 2 the second)
-        if (ok && th == 0 && lane == 0 && (quad == 0 || (NH == 2 && quad == 2)))
-            p.seg_decay[(size_t)slot * p.HV + head + e] = ex2(run);
         if (ok && mine) {
-            const int v = 32 * quad + lane, h = head + v / DV;
-            float4 *dst = reinterpret_cast<float4 *>(p.seg_state + (((size_t)slot * p.HV + h) * DV + v % DV) * DK + 32 * th);
+            const int row = 32 * quad + lane;
+            float4 *dst = reinterpret_cast<float4 *>(
+                p.seg_state + (((size_t)slot * p.HV + head + row / DV) * DV + row % DV) * DK + 32 * th);
 #pragma unroll
             for (int u = 0; u < 8; ++u) dst[u] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
         }
+        // (quadrant 0 has the first head, quadrant 2 the second)
+        if (ok && th == 0 && lane == 0 && (quad == 0 || (NH == 2 && quad == 2)))
+            p.seg_decay[(size_t)slot * p.HV + head + e] = ex2(run);
     }
     __syncthreads();
     if (warp == 2) {
@@ -521,10 +532,13 @@ enum ScBar { B_CF, B_CE, B_BF0, B_BF1, B_BE0, B_BE1, B_XF0, B_XF1, B_XE0, B_XE1,
              B_CB = B_TE0 + 3, B_P, B_S, B_UD, B_WF0, B_WE0 = B_WF0 + 3, B_Y = B_WE0 + 3, B_YE, B_CL, B_DONE, B_COUNT };
 static_assert(8 * B_COUNT + 8 <= 384, "barriers");
 // One head's factors of a chunk: per token the running sum of log2 decays in its
-// 32-token block, delta times the decays behind it in the block, and delta; per block
+// 32-token block, delta times the decays behind it in the block, and `diag`; per block
 // the sum of its log2 decays and the decays behind the block.
+// A block whose decays multiply to no less than 2^-100 (kMild) has delta e^(-running sum)
+// in `diag`: its diagonal tile then needs no exponential per element.  Others have delta.
+constexpr float kMild = -100.f;
 struct HeadTable {
-    float run[L], tail[L], delta[L];
+    float run[L], tail[L], diag[L];
 };
 struct BlockTable {
     float sum[4], behind[4], all;   // (all: the decays of the whole chunk)
@@ -655,7 +669,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             tc_fence_after();
             const uint64_t bd = sdesc_sw128(sb + Cfg::O_B + (c & 1) * 32768, 16, 1024);
             if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
                     mma_bf16(tmem + T_CB, desc_add(cd, off), desc_add(bd, off), id_cb, k > 0);
@@ -680,7 +694,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_bf16(tmem + T_Y1, desc_add(cd, (k >> 2) * 16384 + (k & 3) * 32), desc_add(sd, k * 2048),
                                      id_cs, k > 0);
@@ -709,7 +723,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
 #pragma unroll
                 for (int e = 0; e < NH; ++e) {
                     const uint64_t xd = sdesc_sw128(xtile + e * 16384, 16384, 1024);
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < 8; ++k)
                         mma_bf16_ts(tmem + T_Y2 + DV * e, tmem + T_CB + 32 * (k >> 1) + 8 * (k & 1) + 16 * e,
                                     desc_add(xd, k * 2048), id_px, k > 0);
@@ -761,7 +775,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                     HeadTable *tab = table(c, e);
                     tab->run[32 * q + lane] = pre;
                     tab->tail[32 * q + lane] = delta * ex2(suf);
-                    tab->delta[32 * q + lane] = delta;
+                    tab->diag[32 * q + lane] = sum >= kMild ? delta * ex2(-pre) : delta;
                     if (lane == 0) {
                         block(c, e)->sum[q] = sum;
                         block(c, e)->behind[q] = ex2(behind[e]);
@@ -796,15 +810,17 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                 for (int e = 0; e < NH; ++e) {
                     const HeadTable *t = table(c, e);
                     const float pi = t->run[i];
-                    if (q < w) {
-                        // decays of the tokens behind block q, up to i
+                    const bool mild = block(c, e)->sum[q] >= kMild;
+                    if (q < w || mild) {
+                        // decays of the tokens behind block q, up to i (on the diagonal: from
+                        // the block's start)
                         const BlockTable *b = block(c, e);
                         float s = pi;
                         if (q < 1 && w > 1) s += b->sum[1];
-                        if (q < 2 && w > 2) s += b->sum[2];
+                        if (q < 2 && w > 2 && q < w) s += b->sum[2];
                         const float rf = ex2(s);
                         const float2 rf2 = make_float2(rf, rf);
-                        const float4 *cf = reinterpret_cast<const float4 *>(t->tail + 32 * q);
+                        const float4 *cf = reinterpret_cast<const float4 *>((q < w ? t->tail : t->diag) + 32 * q);
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
                             const float4 f = cf[u];
@@ -813,9 +829,17 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                             out[2 * u] = pack_bf16x2(p0.x, p0.y);
                             out[2 * u + 1] = pack_bf16x2(p1.x, p1.y);
                         }
+                        if (q == w) {
+                            // tokens behind i: the pairs with both, or the second, behind it
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) {
+                                if (2 * u > lane) out[u] = 0u;
+                                if (2 * u == lane) out[u] &= 0xffffu;
+                            }
+                        }
                     } else {
                         const float4 *pj = reinterpret_cast<const float4 *>(t->run + 32 * q);
-                        const float4 *dj = reinterpret_cast<const float4 *>(t->delta + 32 * q);
+                        const float4 *dj = reinterpret_cast<const float4 *>(t->diag + 32 * q);
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
                             const float4 g4 = pj[u], d4 = dj[u];
@@ -870,9 +894,14 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                            pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
                 if (c < last) {
                     const float s = block(c, (32 * g) / DV)->all;
+                    const float2 s2 = make_float2(s, s);
                     uint32_t o[32];
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(v[u] * s);
+                    for (int u = 0; u < 16; ++u) {
+                        const float2 f = mulp(make_float2(v[2 * u], v[2 * u + 1]), s2);
+                        o[2 * u] = __float_as_uint(f.x);
+                        o[2 * u + 1] = __float_as_uint(f.y);
+                    }
                     tmem_st32(ta, o);
                 }
             }
