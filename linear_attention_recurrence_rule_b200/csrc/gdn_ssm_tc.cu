@@ -527,7 +527,7 @@ struct ScanCfg {
     static constexpr uint32_t BYTES = O_BAR + 768 + 1024;
 };
 static_assert(ScanCfg<128, 2>::BYTES <= 232448, "shared memory");
-constexpr int kScMask = 4, kScState = 8, kScWeight = 12, kScOut = 16, kScThreads = 24 * 32;
+constexpr int kScMask = 4, kScState = 8, kScWeight = 12, kScOut = 16, kScThreads = 20 * 32;
 enum ScBar { B_CF, B_CE, B_BF0, B_BF1, B_BE0, B_BE1, B_XF0, B_XF1, B_XE0, B_XE1, B_TF0, B_TE0 = B_TF0 + 3,
              B_CB = B_TE0 + 3, B_P, B_S, B_UD, B_WF0, B_WE0 = B_WF0 + 3, B_Y = B_WE0 + 3, B_YE, B_CL, B_DONE, B_COUNT };
 static_assert(8 * B_COUNT + 8 <= 384, "barriers");
@@ -573,11 +573,11 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             mbar_init(&bars[B_BF0 + i], 1);
             mbar_init(&bars[B_BE0 + i], 1);
             mbar_init(&bars[B_XF0 + i], 1);
-            mbar_init(&bars[B_XE0 + i], 12);
+            mbar_init(&bars[B_XE0 + i], 8);
         }
         for (int i = 0; i < Cfg::NT; ++i) {
             mbar_init(&bars[B_TF0 + i], 1);
-            mbar_init(&bars[B_TE0 + i], 20);
+            mbar_init(&bars[B_TE0 + i], 16);
         }
         mbar_init(&bars[B_CB], 1);
         mbar_init(&bars[B_P], 4);
@@ -588,7 +588,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             mbar_init(&bars[B_WE0 + i], 1);
         }
         mbar_init(&bars[B_Y], 1);
-        mbar_init(&bars[B_YE], 8);
+        mbar_init(&bars[B_YE], 4);
         mbar_init(&bars[B_CL], 4);
         mbar_init(&bars[B_DONE], 1);
         *abort_flag = 0;
@@ -969,21 +969,23 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
         }
     } else if (warp >= kScOut) {
         // ------------------------------------------------ y (rows i = tokens)
-        // half of the columns each: with two heads, a head each
-        const int quad = warp & 3, half = (warp - kScOut) >> 2, i = 32 * quad + lane;
-        const int e = NH == 2 ? half : 0, col0 = half * (VT / 2);
-        const float dh = p.d ? p.d[head + e] : 0.f;
-        const float2 de2 = make_float2(dh, dh);
-        __nv_bfloat16 *yr = p.y + ((seg.t0 + i) * p.HV + head) * DV + col0;
+        const int quad = warp & 3, i = 32 * quad + lane;
+        float dh[NH];
+#pragma unroll
+        for (int e = 0; e < NH; ++e) dh[e] = p.d ? p.d[head + e] : 0.f;
+        __nv_bfloat16 *yr = p.y + ((seg.t0 + i) * p.HV + head) * DV;
         for (int c = 0; c < nch && ok; ++c) {
             ok = table_full(c) && wt(B_XF0 + (c & 1), par2(c));
             if (!ok) break;
-            float s = table(c, e)->run[i];
+            float ga[NH];
 #pragma unroll
-            for (int m = 0; m < 3; ++m)
-                if (m < quad) s += block(c, e)->sum[m];
-            const float ga = ex2(s);
-            const float2 ga2 = make_float2(ga, ga);
+            for (int e = 0; e < NH; ++e) {
+                float s = table(c, e)->run[i];
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    if (m < quad) s += block(c, e)->sum[m];
+                ga[e] = ex2(s);
+            }
             warp_arrive(&bars[B_TE0 + c % 3]);
             ok = wt(B_Y, (uint32_t)(c & 1));
             if (!ok) break;
@@ -991,8 +993,10 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             const bool in = c < last || i < tail;
             const uint32_t xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
 #pragma unroll 1
-            for (int g = 0; g < VT / 32; ++g) {
-                const int col = col0 + 16 * g;
+            for (int g = 0; g < VT / 16; ++g) {
+                const int col = 16 * g;
+                const float gs = NH == 2 && col >= DV ? ga[NH - 1] : ga[0], ds = NH == 2 && col >= DV ? dh[NH - 1] : dh[0];
+                const float2 ga2 = make_float2(gs, gs), de2 = make_float2(ds, ds);
                 float v1[16], v2[16];
                 tmem_ld16(tmem_addr(tmem, warp, T_Y1 + col), v1);
                 tmem_ld16(tmem_addr(tmem, warp, T_Y2 + col), v2);
