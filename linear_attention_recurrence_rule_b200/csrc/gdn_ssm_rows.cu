@@ -5,23 +5,26 @@
 //   S_t = alpha_t S_{t-1} + delta_t x_t b_t^T,   y_t = S_t c_t + d_h x_t
 //
 // The rows of a state (one per value) never mix, so a warp walks the tokens with
-// its rows in registers: a thread holds 4 rows x 8 columns, DK/8 lanes a row.  A
-// token costs a lane 32 multiplies, 32 multiply-adds for the update and 32 for the
-// read-out, done on packed fp32 pairs, and a transposed reduction that leaves each
-// lane one row's sum (5 shuffles for 4 rows).  Tokens come in tiles of 32 by
-// cp.async, one tile ahead.
+// its rows in registers: a thread holds 8 rows x 8 columns, DK/8 lanes a row.  A
+// token costs a lane 64 multiplies and 64 multiply-adds for the update and 64 for the
+// read-out, done on packed fp32 pairs: the instructions issued are what bounds the
+// kernel, so a thread's tile is as large as its registers take (7 shared loads a token
+// for 64 elements; 4 rows took 3.0 instructions per element, 8 take 2.3), and the sums
+// of two tokens x 8 rows are reduced together, transposed (15 shuffles for 16 sums).
+// Tokens come in tiles of 16 by cp.async, one tile ahead.
 //
 // The tokens of a segment follow one another, so one segment per sequence would
 // leave most SMs without work.  The sequence is cut into segments (find_seg): a
 // first pass forms each segment's own state from zero and its decay, combine_kernel
 // chains them, and the second pass runs every segment from its start state.
+#include <type_traits>
+
 #include "gdn_ssm_common.cuh"
 
 namespace gdn {
 namespace ssm {
 
-constexpr int kTile = 32;        // tokens per tile
-constexpr int kRows = 4;         // state rows per thread
+constexpr int kTile = 16;        // tokens per tile
 constexpr int kCols = 8;         // state columns per thread
 
 struct RowParams {
@@ -76,24 +79,47 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 
-template <int DK>
-__host__ __device__ constexpr int rows_per_warp() { return 32 / (DK / kCols) * kRows; }
+// ROWS state rows per thread: 8 (4 where a warp of 8 would have more rows than the head), or
+// 2 where there is too little to do to fill the SMs and a token's latency counts
+template <int DK, int ROWS>
+__host__ __device__ constexpr int rows_per_warp() { return 32 / (DK / kCols) * ROWS; }
 
-// one tile of raw tokens
+// v[N] summed over the W lanes of a row group: halves the values while it halves the
+// lanes.  `first`: the index of the value now in v[0] (then v[1], ... follow it).
+template <int N, int W>
+__device__ __forceinline__ void reduce(float *v, int lane, int &first) {
+    if constexpr (W > 1) {
+        if constexpr (N > 1) {
+            const bool up = (lane & (W / 2)) != 0;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float keep = up ? v[N / 2 + i] : v[i], send = up ? v[i] : v[N / 2 + i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, W / 2);
+            }
+            if (up) first += N / 2;
+            reduce<N / 2, W / 2>(v, lane, first);
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], W / 2);
+            reduce<1, W / 2>(v, lane, first);
+        }
+    }
+}
+
+// one tile of raw tokens; `rows` values of x each
 template <int DK, typename T>
 struct Tile {
     T b[kTile][DK];
     T c[kTile][DK];
     T x[kTile][128];
-    float delta[kTile], alpha[kTile];
+    float2 step[kTile];     // delta, alpha
 };
 
 // READ: the second pass (start states, read-out, final state); otherwise the first
-template <int DK, typename T, bool READ>
-__global__ void __launch_bounds__(128)
+template <int DK, int ROWS, typename T, bool READ>
+__global__ void __launch_bounds__(128, ROWS == 8 ? 4 : ROWS == 4 ? 7 : 8)
 scan_rows_kernel(const RowParams p) {
     constexpr int LPR = DK / kCols;          // lanes per row group
-    constexpr int RPW = rows_per_warp<DK>();
+    constexpr int RPW = rows_per_warp<DK, ROWS>();
     constexpr int V = 16 / (int)sizeof(T);   // elements per 16 bytes
     extern __shared__ __align__(16) uint8_t raw[];
     Tile<DK, T> *tiles = reinterpret_cast<Tile<DK, T> *>(raw);
@@ -109,7 +135,7 @@ scan_rows_kernel(const RowParams p) {
     const int h = hb / bands, row0 = (hb - h * bands) * rpc;
     const int ck = h / (p.HV / p.HK);
     const int l = lane % LPR, grp = lane / LPR;
-    const int lrow = warp * RPW + grp * kRows;        // first row of this thread in the CTA
+    const int lrow = warp * RPW + grp * ROWS;        // first row of this thread in the CTA
     const T *xp = static_cast<const T *>(p.x) + seg.t0 * p.x_row + (int64_t)h * p.dv + row0;
     const T *bp = static_cast<const T *>(p.b) + seg.t0 * p.b_row + (int64_t)ck * DK;
     const T *cp = static_cast<const T *>(p.c) + seg.t0 * p.c_row + (int64_t)ck * DK;
@@ -119,11 +145,11 @@ scan_rows_kernel(const RowParams p) {
     const size_t st = ((size_t)slot * p.HV + h) * p.dv * DK;      // this segment's slot
     const size_t sq = ((size_t)seg.n * p.HV + h) * p.dv * DK;           // this sequence's state
 
-    float2 S[kRows][4];
+    float2 S[ROWS][4];
     const float *src = nullptr;
     if (READ) src = p.chained ? p.seg_state + st : p.h0 ? p.h0 + sq : nullptr;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -150,8 +176,7 @@ scan_rows_kernel(const RowParams p) {
             }
             for (int i = tid; i < m; i += nt) {
                 const float dl = step_size(dtp[(at + i) * p.HV], bias, p.softplus);
-                t.delta[i] = dl;
-                t.alpha[i] = expf(dl * ah);
+                t.step[i] = make_float2(dl, expf(dl * ah));
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -165,61 +190,70 @@ scan_rows_kernel(const RowParams p) {
         const Tile<DK, T> &t = tiles[k & 1];
         const int m = min(kTile, seg.len - k * kTile);
         T *yo = READ ? static_cast<T *>(p.y) + ((seg.t0 + (int64_t)k * kTile) * p.HV + h) * p.dv + row0 : nullptr;
-        for (int i = 0; i < m; ++i) {
-            float2 bb[4];
-            load_cols(t.b[i], l, DK, bb);
-            const float al = t.alpha[i], dl = t.delta[i];
-            const float2 al2 = make_float2(al, al);
-            float xr[kRows], acc[kRows];
-            {
-                const float4 f = load4(&t.x[i][lrow]);
-                xr[0] = f.x;
-                xr[1] = f.y;
-                xr[2] = f.z;
-                xr[3] = f.w;
-            }
+        // U tokens from token i
+        auto tokens = [&](auto count, int i) {
+            constexpr int U = decltype(count)::value;
+            float acc[U * ROWS], xr[U * ROWS];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float u = dl * xr[r];
-                const float2 u2 = make_float2(u, u);
+            for (int u = 0; u < U; ++u) {
+                float2 bb[4], cc[4];
+                load_cols(t.b[i + u], l, DK, bb);
+                if (READ) load_cols(t.c[i + u], l, DK, cc);
+                const float2 step = t.step[i + u];
+                const float2 al2 = make_float2(step.y, step.y);
+                if constexpr (ROWS >= 4) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) S[r][j] = fma2(S[r][j], al2, mul2(u2, bb[j]));
+                    for (int r = 0; r < ROWS; r += 4) {
+                        const float4 f = load4(&t.x[i + u][lrow + r]);
+                        xr[u * ROWS + r] = f.x;
+                        xr[u * ROWS + r + 1] = f.y;
+                        xr[u * ROWS + r + 2] = f.z;
+                        xr[u * ROWS + r + 3] = f.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) xr[u * ROWS + r] = to_f32(t.x[i + u][lrow + r]);
+                }
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    const float w = step.x * xr[u * ROWS + r];
+                    const float2 w2 = make_float2(w, w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[r][j] = fma2(S[r][j], al2, mul2(w2, bb[j]));
+                    if (READ) {
+                        float2 s2 = mul2(S[r][0], cc[0]);
+#pragma unroll
+                        for (int j = 1; j < 4; ++j) s2 = fma2(S[r][j], cc[j], s2);
+                        acc[u * ROWS + r] = s2.x + s2.y;
+                    }
+                }
+                if (!READ) decay *= step.y;
             }
             if (READ) {
-                float2 cc[4];
-                load_cols(t.c[i], l, DK, cc);
+                int first = 0;
+                reduce<U * ROWS, LPR>(acc, lane, first);
+                // values left per lane; fewer values than lanes: the lanes with low bits 0 write
+                constexpr int M = U * ROWS / LPR > 0 ? U * ROWS / LPR : 1;
+                constexpr int IDLE = LPR / (U * ROWS) > 0 ? LPR / (U * ROWS) : 1;
+                if ((lane & (IDLE - 1)) == 0) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    float2 s2 = mul2(S[r][0], cc[0]);
-#pragma unroll
-                    for (int j = 1; j < 4; ++j) s2 = fma2(S[r][j], cc[j], s2);
-                    acc[r] = s2.x + s2.y;
+                    for (int q = 0; q < M; ++q) {
+                        const int id = first + q, u = id / ROWS, r = id % ROWS;
+                        const float xv = to_f32(t.x[i + u][lrow + r]);
+                        yo[(int64_t)(i + u) * p.HV * p.dv + lrow + r] = from_f32<T>(fmaf(dh, xv, acc[q]));
+                    }
                 }
-                // 4 rows over LPR lanes: halve the rows twice, then plain butterflies
-                const bool up = (lane & (LPR / 2)) != 0;
-                float k0 = up ? acc[2] : acc[0], k1 = up ? acc[3] : acc[1];
-                k0 += __shfl_xor_sync(0xffffffffu, up ? acc[0] : acc[2], LPR / 2);
-                k1 += __shfl_xor_sync(0xffffffffu, up ? acc[1] : acc[3], LPR / 2);
-                const bool up2 = (lane & (LPR / 4)) != 0;
-                float v = up2 ? k1 : k0;
-                v += __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, LPR / 4);
-#pragma unroll
-                for (int off = LPR / 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                if ((lane & (LPR / 4 - 1)) == 0) {
-                    const int r = (up ? 2 : 0) + (up2 ? 1 : 0);
-                    const float xv = up ? (up2 ? xr[3] : xr[2]) : (up2 ? xr[1] : xr[0]);
-                    yo[(int64_t)i * p.HV * p.dv + lrow + r] = from_f32<T>(fmaf(dh, xv, v));
-                }
-            } else {
-                decay *= al;
             }
-        }
+        };
+        int i = 0;
+        for (; i + 2 <= m; i += 2) tokens(std::integral_constant<int, 2>{}, i);
+        if (i < m) tokens(std::integral_constant<int, 1>{}, i);
         __syncthreads();
     }
     float *dst = READ ? (seg.last && p.hT ? p.hT + sq : nullptr) : p.seg_state + st;
     if (dst) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 *reinterpret_cast<float4 *>(dst + (size_t)(row0 + lrow + r) * DK + col_of<DK, T>(l, q)) =
@@ -343,29 +377,31 @@ struct Cut {
     size_t table, first, decay, state, total;   // byte offsets in the workspace
 };
 
+// warps per CTA of a head with `rows` rows per thread
+static int warps_of(int dk, int dv, int rows) { return min(4, dv / (32 / (dk / kCols) * rows)); }
+static int full_rows(int dk, int dv) { return 32 / (dk / kCols) * 8 <= dv ? 8 : 4; }
 static int ctas_per_state(const SsmArgs &a) {
-    const int rpw = a.dk == 128 ? rows_per_warp<128>() : a.dk == 64 ? rows_per_warp<64>() : rows_per_warp<32>();
-    const int warps = min(4, max(1, a.dv / rpw));
-    return a.dv / (warps * rpw);
+    const int rows = full_rows(a.dk, a.dv);
+    return a.dv / (warps_of(a.dk, a.dv, rows) * 32 / (a.dk / kCols) * rows);
 }
 
-// Segments are worth their first pass (2/5 of the second's arithmetic) while the SMs
-// have fewer than about 3 CTAs of 4 warps each without them; below 256 tokens a
-// segment's start and end states weigh as much as its tokens.
+// Segments are worth their first pass (half of the second's arithmetic) while the SMs have
+// fewer than about 4 CTAs of 4 warps each without them; below 128 tokens a segment's start
+// and end states weigh as much as its tokens.
 static Cut cut_rows(const SsmArgs &a) {
     Cut c{};
     const bool packed = a.cu_seqlens != nullptr;
     const int64_t longest = a.T > 0 ? a.T : 1;
     const int64_t base = (int64_t)a.HV * ctas_per_state(a) * (packed ? 1 : a.N);
-    int64_t nseg = base >= 444 ? 1 : (444 + base - 1) / base;
+    int64_t nseg = base >= 592 ? 1 : 592 / base;
     int64_t len = (longest + nseg - 1) / nseg;
     len = (len + kTile - 1) / kTile * kTile;
-    if (len < 256) len = 256;
+    if (len < 128) len = 128;
     if (len > (1 << 30)) len = 1 << 30;
     c.seg_len = (int)len;
     c.nseg = (int)((longest + len - 1) / len);
     const int64_t bound = packed ? a.T / len + a.N : (int64_t)a.N * c.nseg;
-    c.bound = bound * a.HV * ctas_per_state(a) > 0x7fffffff ? -1 : (int)bound;   // grid.x
+    c.bound = bound * a.HV * 4 > 0x7fffffff ? -1 : (int)bound;   // grid.x
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     size_t off = 256;
     c.table = off;
@@ -383,8 +419,8 @@ static Cut cut_rows(const SsmArgs &a) {
     return c;
 }
 
-template <int DK, typename T>
-static cudaError_t launch_rows(const SsmArgs &a, cudaStream_t stream) {
+template <int DK, int ROWS, typename T>
+static cudaError_t launch_rows_of(const SsmArgs &a, cudaStream_t stream) {
     const Cut cut = cut_rows(a);
     if (cut.bound < 0) return cudaErrorInvalidValue;
     cudaError_t err = cudaSuccess;
@@ -407,25 +443,36 @@ static cudaError_t launch_rows(const SsmArgs &a, cudaStream_t stream) {
                           reinterpret_cast<int *>(ws + cut.first), stream);
         if (err != cudaSuccess) return err;
     }
-    const int warps = min(4, max(1, a.dv / rows_per_warp<DK>()));
+    const int warps = warps_of(DK, a.dv, ROWS);
     const dim3 block(32 * warps);
-    const int bands = a.dv / (warps * rows_per_warp<DK>());
+    const int bands = a.dv / (warps * rows_per_warp<DK, ROWS>());
     constexpr size_t smem = 2 * sizeof(Tile<DK, T>);
     const dim3 grid((unsigned)((int64_t)cut.bound * a.HV * bands));
     const bool cuts = packed ? a.T > cut.seg_len : cut.nseg > 1;
     if (cuts) {
         p.chained = true;
-        err = cudaFuncSetAttribute(scan_rows_kernel<DK, T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        err = cudaFuncSetAttribute(scan_rows_kernel<DK, ROWS, T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
-        scan_rows_kernel<DK, T, false><<<grid, block, smem, stream>>>(p);
+        scan_rows_kernel<DK, ROWS, T, false><<<grid, block, smem, stream>>>(p);
         err = launch_combine(p.seg_state, p.seg_decay, a.h0, nullptr, a.N, a.HV, a.dv * DK, false, p.map, stream);
         if (err != cudaSuccess) return err;
     }
-    err = cudaFuncSetAttribute(scan_rows_kernel<DK, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    err = cudaFuncSetAttribute(scan_rows_kernel<DK, ROWS, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    if (cuts) return launch_after(scan_rows_kernel<DK, T, true>, grid, block, smem, stream, p);
-    scan_rows_kernel<DK, T, true><<<grid, block, smem, stream>>>(p);
+    if (cuts) return launch_after(scan_rows_kernel<DK, ROWS, T, true>, grid, block, smem, stream, p);
+    scan_rows_kernel<DK, ROWS, T, true><<<grid, block, smem, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int DK, typename T>
+static cudaError_t launch_rows(const SsmArgs &a, cudaStream_t stream) {
+    // fewer than a warp per scheduler: 2 rows per thread (128 tokens, 2 heads of 32: 37 -> 21 us)
+    const Cut cut = cut_rows(a);
+    const int64_t warps = (int64_t)cut.bound * a.HV * ctas_per_state(a) * warps_of(DK, a.dv, full_rows(DK, a.dv));
+    if (warps < 592) return launch_rows_of<DK, 2, T>(a, stream);
+    if constexpr (DK == 32)
+        if (full_rows(DK, a.dv) == 4) return launch_rows_of<DK, 4, T>(a, stream);
+    return launch_rows_of<DK, 8, T>(a, stream);
 }
 
 }  // namespace ssm
