@@ -13,6 +13,15 @@
 // of two tokens x 8 rows are reduced together, transposed (15 shuffles for 16 sums).
 // Tokens come in tiles of 16 by cp.async, one tile ahead.
 //
+// What bounds it is the fp32 multiply-add rate (packed pairs save instructions, not
+// rate), so a tile whose decays multiply to no less than 2^-60 -- nearly every one -- is
+// run on the state divided by its decays since the tile's start: with
+// Gamma_t = alpha_1 .. alpha_t,  S'_t = S'_{t-1} + (delta_t / Gamma_t) x_t b_t^T  and
+// y_t = Gamma_t S'_t c_t + d x_t, two operations per element and token instead of three,
+// and one instead of two in the first pass; the state is multiplied by the tile's decay
+// once at its end.  Nothing overflows within 2^60, and a sum keeps its relative accuracy
+// whatever it is divided by.  Stronger tiles take the plain form.
+//
 // The tokens of a segment follow one another, so one segment per sequence would
 // leave most SMs without work.  The sequence is cut into segments (find_seg): a
 // first pass forms each segment's own state from zero and its decay, combine_kernel
@@ -26,6 +35,7 @@ namespace ssm {
 
 constexpr int kTile = 16;        // tokens per tile
 constexpr int kCols = 8;         // state columns per thread
+constexpr float kMildTile = 0x1p-60f;
 
 struct RowParams {
     const void *x, *b, *c;
@@ -105,13 +115,14 @@ __device__ __forceinline__ void reduce(float *v, int lane, int &first) {
     }
 }
 
-// one tile of raw tokens; `rows` values of x each
+// one tile of raw tokens (16-byte copies and reads: so is the second tile's start)
 template <int DK, typename T>
-struct Tile {
+struct alignas(16) Tile {
     T b[kTile][DK];
     T c[kTile][DK];
     T x[kTile][128];
-    float2 step[kTile];     // delta, alpha
+    float2 step[kTile];     // delta_t / Gamma_t, Gamma_t (mild) or delta_t, alpha_t
+    float total;            // the tile's decay where it is mild, else 0
 };
 
 // READ: the second pass (start states, read-out, final state); otherwise the first
@@ -174,9 +185,20 @@ scan_rows_kernel(const RowParams p) {
                 const int r = i / xv, e = (i - r * xv) * V;
                 cp16(&t.x[r][e], xp + (at + r) * p.x_row + e);
             }
-            for (int i = tid; i < m; i += nt) {
-                const float dl = step_size(dtp[(at + i) * p.HV], bias, p.softplus);
-                t.step[i] = make_float2(dl, expf(dl * ah));
+            if (warp == 0) {
+                const bool in = lane < m;
+                const float dl = in ? step_size(dtp[(at + lane) * p.HV], bias, p.softplus) : 0.f;
+                const float al = in ? expf(dl * ah) : 1.f;
+                float gamma = al;
+#pragma unroll
+                for (int off = 1; off < kTile; off <<= 1) {
+                    const float v = __shfl_up_sync(0xffffffffu, gamma, off);
+                    if (lane >= off) gamma *= v;
+                }
+                const float total = __shfl_sync(0xffffffffu, gamma, kTile - 1);
+                const bool mild = total >= kMildTile;
+                if (lane < kTile) t.step[lane] = mild ? make_float2(dl / gamma, gamma) : make_float2(dl, al);
+                if (lane == 0) t.total = mild ? total : 0.f;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -191,8 +213,9 @@ scan_rows_kernel(const RowParams p) {
         const int m = min(kTile, seg.len - k * kTile);
         T *yo = READ ? static_cast<T *>(p.y) + ((seg.t0 + (int64_t)k * kTile) * p.HV + h) * p.dv + row0 : nullptr;
         // U tokens from token i
-        auto tokens = [&](auto count, int i) {
+        auto tokens = [&](auto count, auto kind, int i) {
             constexpr int U = decltype(count)::value;
+            constexpr bool MILD = decltype(kind)::value;
             float acc[U * ROWS], xr[U * ROWS];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -219,7 +242,7 @@ scan_rows_kernel(const RowParams p) {
                     const float w = step.x * xr[u * ROWS + r];
                     const float2 w2 = make_float2(w, w);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) S[r][j] = fma2(S[r][j], al2, mul2(w2, bb[j]));
+                    for (int j = 0; j < 4; ++j) S[r][j] = MILD ? fma2(w2, bb[j], S[r][j]) : fma2(S[r][j], al2, mul2(w2, bb[j]));
                     if (READ) {
                         float2 s2 = mul2(S[r][0], cc[0]);
 #pragma unroll
@@ -227,7 +250,7 @@ scan_rows_kernel(const RowParams p) {
                         acc[u * ROWS + r] = s2.x + s2.y;
                     }
                 }
-                if (!READ) decay *= step.y;
+                if (!READ && !MILD) decay *= step.y;
             }
             if (READ) {
                 int first = 0;
@@ -240,14 +263,30 @@ scan_rows_kernel(const RowParams p) {
                     for (int q = 0; q < M; ++q) {
                         const int id = first + q, u = id / ROWS, r = id % ROWS;
                         const float xv = to_f32(t.x[i + u][lrow + r]);
-                        yo[(int64_t)(i + u) * p.HV * p.dv + lrow + r] = from_f32<T>(fmaf(dh, xv, acc[q]));
+                        const float v = MILD ? acc[q] * t.step[i + u].y : acc[q];
+                        yo[(int64_t)(i + u) * p.HV * p.dv + lrow + r] = from_f32<T>(fmaf(dh, xv, v));
                     }
                 }
             }
         };
-        int i = 0;
-        for (; i + 2 <= m; i += 2) tokens(std::integral_constant<int, 2>{}, i);
-        if (i < m) tokens(std::integral_constant<int, 1>{}, i);
+        auto tile = [&](auto kind) {
+            int i = 0;
+#pragma unroll 1
+            for (; i + 2 <= m; i += 2) tokens(std::integral_constant<int, 2>{}, kind, i);
+            if (i < m) tokens(std::integral_constant<int, 1>{}, kind, i);
+        };
+        const float total = t.total;
+        if (total > 0.f) {
+            tile(std::true_type{});
+            const float2 t2 = make_float2(total, total);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[r][j] = mul2(S[r][j], t2);
+            if (!READ) decay *= total;
+        } else {
+            tile(std::false_type{});
+        }
         __syncthreads();
     }
     float *dst = READ ? (seg.last && p.hT ? p.hT + sq : nullptr) : p.seg_state + st;
@@ -447,6 +486,7 @@ static cudaError_t launch_rows_of(const SsmArgs &a, cudaStream_t stream) {
     const dim3 block(32 * warps);
     const int bands = a.dv / (warps * rows_per_warp<DK, ROWS>());
     constexpr size_t smem = 2 * sizeof(Tile<DK, T>);
+    static_assert(sizeof(Tile<DK, T>) % 16 == 0, "tile alignment");
     const dim3 grid((unsigned)((int64_t)cut.bound * a.HV * bands));
     const bool cuts = packed ? a.T > cut.seg_len : cut.nseg > 1;
     if (cuts) {
