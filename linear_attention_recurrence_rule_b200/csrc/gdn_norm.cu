@@ -79,11 +79,20 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&f)[N])
         *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
-// the gate's factor: full precision for fp32 results, the layer steps' fast sigmoid
-// (relative error ~1e-6) for bf16 ones
+// the gate's factor: full precision for fp32 results, the hardware's exponential and
+// reciprocal for bf16 ones (relative error about 1e-6 beside a rounding of 2^-8).  Four
+// instructions for the sigmoid: with the layer steps' clamped division, 37 instructions an
+// element kept a 4096 x 32 x 128 call from memory speed.
 template <typename T>
 __device__ __forceinline__ float gate_factor(float z, bool silu) {
-    const float s = sizeof(T) == 4 ? gate_sigmoid(z) : layer_sigmoid(z);
+    float s;
+    if constexpr (sizeof(T) == 4) {
+        s = gate_sigmoid(z);
+    } else {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    }
     return silu ? z * s : s;
 }
 
@@ -103,60 +112,105 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
     return v;
 }
 
-__device__ __forceinline__ float inv_rms(float ss, int D, float eps) { return rsqrtf(ss / (float)D + eps); }
+// (mean = ss / D as a product with 1 / D: one more rounding of 2^-24)
+__device__ __forceinline__ float inv_rms(float ss, float inv_d, float eps) { return rsqrtf(fmaf(ss, inv_d, eps)); }
+
+// Quotient by a divisor known on the host, exact for dividends below 2^31: with
+// 2^(k-1) < d <= 2^k and m = ceil(2^(31+k) / d), q = n m / 2^(31+k).
+struct Divisor {
+    uint32_t m;
+    int shift;
+};
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor &d) {
+    return (uint32_t)(((uint64_t)n * d.m) >> d.shift);
+}
+Divisor divisor(uint32_t d) {
+    int k = 0;
+    while (k < 31 && (1u << k) < d) ++k;
+    return {(uint32_t)(((1ull << (31 + k)) + d - 1) / d), 31 + k};
+}
 
 constexpr int kSmallThreads = 256;   // block of the kernels with several rows per warp
 
-template <typename T, int TPR, int NV>
+// 16 bytes of one dtype, raw, as floats
+template <typename T>
+__device__ __forceinline__ void to_floats(const uint4 &u, float (&f)[Vec<T>::n]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            f[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+
+template <typename T, int TPR, int NV, bool FIRST>
 __global__ void __launch_bounds__(TPR > 32 ? TPR : kSmallThreads)
-gated_norm_kernel(const GatedNormArgs a) {
+gated_norm_kernel(const GatedNormArgs a, const Divisor groups, const float inv_d) {
     constexpr int VN = Vec<T>::n;
-    constexpr int RPB = TPR > 32 ? 1 : kSmallThreads / TPR;
+    constexpr int RPB = (TPR > 32 ? 1 : kSmallThreads / TPR);
     __shared__ float part[32];
-    const int64_t unit = (int64_t)blockIdx.x * RPB + (TPR > 32 ? 0 : threadIdx.x / TPR);
+    // (fewer than 2^31 groups: 32-bit indexes)
+    const uint32_t unit = blockIdx.x * (uint32_t)RPB + (TPR > 32 ? 0 : threadIdx.x / TPR);
     const int lane = TPR > 32 ? threadIdx.x : threadIdx.x % TPR;
-    const bool live = unit < a.rows * a.G;
-    const int64_t r = live ? unit / a.G : 0;
-    const int g = live ? (int)(unit - r * a.G) : 0;
-    const T *o = static_cast<const T *>(a.o) + r * a.o_row + (int64_t)g * a.D;
-    const T *z = a.z ? static_cast<const T *>(a.z) + r * a.z_row + (int64_t)g * a.D : nullptr;
-    T *y = static_cast<T *>(a.y) + (r * a.G + g) * a.D;
+    const uint32_t G = (uint32_t)a.G;
+    const bool live = unit < (uint32_t)(a.rows * a.G);
+    const uint32_t r = live ? quotient(unit, groups) : 0u, g = live ? unit - r * G : 0u;
+    const int64_t col = (int64_t)g * a.D;
+    const T *o = static_cast<const T *>(a.o) + r * a.o_row + col;
+    const T *z = static_cast<const T *>(a.z) + r * a.z_row + col;
+    uint4 uo[NV], uz[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int e = (k * TPR + lane) * VN;
+        if (live && e < a.D) {
+            uo[k] = *reinterpret_cast<const uint4 *>(o + e);
+            if (a.z) uz[k] = *reinterpret_cast<const uint4 *>(z + e);
+        }
+    }
     float u[NV][VN], f[NV][VN];
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int e = (k * TPR + lane) * VN;
-        if (live && e < a.D) {
-            load_vec<VN>(o + e, u[k]);
-            if (z) load_vec<VN>(z + e, f[k]);
-        }
-    }
+        if (live && (k * TPR + lane) * VN < a.D) {
+            to_floats<T>(uo[k], u[k]);
+            if (a.z) {
+                to_floats<T>(uz[k], f[k]);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int e = (k * TPR + lane) * VN;
-        if (live && e < a.D) {
+                for (int i = 0; i < VN; ++i) f[k][i] = gate_factor<T>(f[k][i], a.silu);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VN; ++i) f[k][i] = 1.f;
+            }
 #pragma unroll
             for (int i = 0; i < VN; ++i) {
-                f[k][i] = z ? gate_factor<T>(f[k][i], a.silu) : 1.f;
-                if (a.gate_first) u[k][i] *= f[k][i];
+                if (FIRST) u[k][i] *= f[k][i];
                 ss = fmaf(u[k][i], u[k][i], ss);
             }
         }
     }
-    const float inv = inv_rms(row_sum<TPR>(ss, part), a.D, a.eps);
-    const float *w = a.weight ? a.weight + (a.weight_per_group ? (int64_t)g * a.D : 0) : nullptr;
+    const float inv = inv_rms(row_sum<TPR>(ss, part), inv_d, a.eps), one = a.unit_offset ? 1.f : 0.f;
+    const float *w = a.weight ? a.weight + (a.weight_per_group ? col : 0) : nullptr;
+    T *y = static_cast<T *>(a.y) + (int64_t)unit * a.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = (k * TPR + lane) * VN;
         if (live && e < a.D) {
-            float wv[VN];
-            if (w) load_vec<VN>(w + e, wv);
+            if (w) {
+                float wv[VN];
+                load_vec<VN>(w + e, wv);
 #pragma unroll
-            for (int i = 0; i < VN; ++i) {
-                const float wi = w ? (a.unit_offset ? 1.f + wv[i] : wv[i]) : 1.f;
-                const float v = u[k][i] * inv * wi;
-                u[k][i] = a.gate_first ? v : v * f[k][i];
+                for (int i = 0; i < VN; ++i) u[k][i] *= inv * (wv[i] + one);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VN; ++i) u[k][i] *= inv;
             }
+#pragma unroll
+            for (int i = 0; i < VN; ++i)
+                if (!FIRST) u[k][i] *= f[k][i];
             store_vec<VN>(y + e, u[k]);
         }
     }
@@ -164,7 +218,7 @@ gated_norm_kernel(const GatedNormArgs a) {
 
 template <typename T, typename TR, int TPR, int NV>
 __global__ void __launch_bounds__(TPR > 32 ? TPR : kSmallThreads)
-residual_norm_kernel(const ResidualNormArgs a) {
+residual_norm_kernel(const ResidualNormArgs a, const float inv_c) {
     constexpr int VN = Vec<T>::n;
     constexpr int RPB = TPR > 32 ? 1 : kSmallThreads / TPR;
     __shared__ float part[2][32];
@@ -191,7 +245,7 @@ residual_norm_kernel(const ResidualNormArgs a) {
             if (live && (k * TPR + lane) * VN < a.C)
 #pragma unroll
                 for (int i = 0; i < VN; ++i) ss = fmaf(t[k][i], t[k][i], ss);
-        const float inv = inv_rms(row_sum<TPR>(ss, part[0]), a.C, a.eps);
+        const float inv = inv_rms(row_sum<TPR>(ss, part[0]), inv_c, a.eps);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int e = (k * TPR + lane) * VN;
@@ -223,7 +277,7 @@ residual_norm_kernel(const ResidualNormArgs a) {
         }
     }
     if (!a.y) return;
-    const float inv = inv_rms(row_sum<TPR>(ss, part[1]), a.C, a.eps);
+    const float inv = inv_rms(row_sum<TPR>(ss, part[1]), inv_c, a.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = (k * TPR + lane) * VN;
@@ -260,7 +314,7 @@ gated_norm_odd_kernel(const GatedNormArgs a) {
         if (z && a.gate_first) u *= gate_factor<T>(to_f32(z[e]), a.silu);
         ss = fmaf(u, u, ss);
     }
-    const float inv = inv_rms(block_sum(ss, part), a.D, a.eps);
+    const float inv = inv_rms(block_sum(ss, part), 1.f / (float)a.D, a.eps);
     const float *w = a.weight ? a.weight + (a.weight_per_group ? (int64_t)g * a.D : 0) : nullptr;
     for (int e = threadIdx.x; e < a.D; e += kOddThreads) {
         float u = to_f32(o[e]);
@@ -288,7 +342,7 @@ residual_norm_odd_kernel(const ResidualNormArgs a) {
             const float u = to_f32(x[e]);
             ss = fmaf(u, u, ss);
         }
-        inv = inv_rms(block_sum(ss, part), a.C, a.eps);
+        inv = inv_rms(block_sum(ss, part), 1.f / (float)a.C, a.eps);
     }
     auto h_of = [&](int e) {
         float t = to_f32(x[e]);
@@ -303,7 +357,7 @@ residual_norm_odd_kernel(const ResidualNormArgs a) {
             const float h = h_of(e);
             ss = fmaf(h, h, ss);
         }
-        inv2 = inv_rms(block_sum(ss, part), a.C, a.eps);
+        inv2 = inv_rms(block_sum(ss, part), 1.f / (float)a.C, a.eps);
     }
     // residual_out may be the residual, y may be x: each element is read before it is written
     for (int e = threadIdx.x; e < a.C; e += kOddThreads) {
@@ -320,9 +374,10 @@ bool vec_ok(const void *p, int64_t row, int elt) {
 // Threads per row and vectors per thread by the row's number of 16-byte vectors
 template <typename F>
 cudaError_t by_vectors(int nv, F f) {
+    // (two vectors a thread from 9 on: what a thread does once weighs less per element)
     if (nv <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-    if (nv <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    if (nv <= 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+    if (nv <= 16) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+    if (nv <= 32) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
     if (nv <= 64) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
     if (nv <= 128) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
     if (nv <= 256) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
@@ -348,8 +403,9 @@ cudaError_t gated_norm(const GatedNormArgs &a, cudaStream_t stream) {
     }
     return by_vectors(a.D / VN, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-        gated_norm_kernel<T, TPR, NV><<<(unsigned)blocks_of(units, TPR), TPR > 32 ? TPR : kSmallThreads, 0,
-                                        stream>>>(a);
+        auto kern = a.gate_first ? gated_norm_kernel<T, TPR, NV, true> : gated_norm_kernel<T, TPR, NV, false>;
+        kern<<<(unsigned)blocks_of(units, TPR), TPR > 32 ? TPR : kSmallThreads, 0, stream>>>(a, divisor((uint32_t)a.G),
+                                                                                           1.f / (float)a.D);
         return cudaGetLastError();
     });
 }
@@ -367,7 +423,7 @@ cudaError_t residual_norm(const ResidualNormArgs &a, cudaStream_t stream) {
     return by_vectors(a.C / VN, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
         residual_norm_kernel<T, TR, TPR, NV><<<(unsigned)blocks_of(a.rows, TPR),
-                                               TPR > 32 ? TPR : kSmallThreads, 0, stream>>>(a);
+                                               TPR > 32 ? TPR : kSmallThreads, 0, stream>>>(a, 1.f / (float)a.C);
         return cudaGetLastError();
     });
 }

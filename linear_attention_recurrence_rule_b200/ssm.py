@@ -271,7 +271,7 @@ def gdn_gated_norm(o, z=None, weight=None, eps: float = 1e-6, gate: str = "sigmo
     o_row = _rows(o, "o", 2)
     y_p = None if y is None else _check(y, "y", o.shape, o.dtype, dev)
     if y is None:
-        y = o.new_empty(o.shape)
+        y = torch.empty_like(o) if o_row == 0 else o.new_empty(o.shape)
         y_p = y.data_ptr()
     n = o.numel()
     if n == 0:
@@ -317,11 +317,11 @@ def gdn_residual_norm(x, residual=None, weight=None, post_weight=None, z=None, s
     pw_p = _opt(post_weight, "post_weight", (C,), f32, dev)
     ro_p = _opt(residual_out, "residual_out", shape, rdtype, dev)
     if residual_out is None:
-        residual_out = kept.new_empty(shape)
+        residual_out = torch.empty_like(kept)
         ro_p = residual_out.data_ptr()
     y_p = None if y is None else _check(y, "y", shape, x.dtype, dev)
     if y is None:
-        y = x.new_empty(shape)
+        y = torch.empty_like(x)
         y_p = y.data_ptr()
     n = x.numel()
     if n == 0:
