@@ -72,6 +72,20 @@ GDN_API int gdn_selftest_verify_tc_timeout(const void *v, const float *state, in
                                            int HV, void *o, float *u_out, void *workspace,
                                            size_t workspace_bytes, gdn_stream_t stream);
 
+/*
+ * Test-only call of the tensor-core state space scan (bf16, dk = 128, dv 64 or 128;
+ * softplus, no d, dt_bias, h0; layouts as gdn_ssm_prefill, dense) in which the warp that
+ * issues the products starts as if its first wait had given up: every wait for one of
+ * them then gives up too (the flag is set, so none waits long), the status word in
+ * `workspace` becomes GDN_ERR_TIMEOUT, the kernels wait for their own loads in flight,
+ * free their tensor memory and return.  y and hT are then undefined.  workspace:
+ * gdn_ssm_prefill_workspace_size(...) bytes.
+ */
+GDN_API int gdn_selftest_ssm_timeout(const void *x, const void *b, const void *c, const float *dt,
+                                     const float *a, int N, int64_t T, int HK, int HV, int dv,
+                                     void *y, float *hT, void *workspace, size_t workspace_bytes,
+                                     gdn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -169,6 +169,7 @@ struct SsmArgs {
     float *hT;
     void *workspace;
     size_t workspace_bytes;
+    bool timeout_test = false;        // test only: the tensor-core kernels' first wait gives up
 };
 struct SsmStepArgs {
     const void *xbc;                  // [N][HV*dv + 2*HK*dk], rows xbc_row apart

@@ -258,3 +258,37 @@ extern "C" int gdn_selftest_verify_tc_timeout(const void *v, const float *state,
     const cudaError_t err = gdn::launch_verify_tc_timeout_test(a, reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
+
+// Test-only state space scan on tensor cores whose waits give up at once (see gdn_selftest.h).
+extern "C" int gdn_selftest_ssm_timeout(const void *x, const void *b, const void *c, const float *dt,
+                                        const float *a, int N, int64_t T, int HK, int HV, int dv, void *y,
+                                        float *hT, void *workspace, size_t workspace_bytes,
+                                        gdn_stream_t stream) {
+    if (!x || !b || !c || !dt || !a || !y || !hT || !workspace) return GDN_ERR_INVALID_ARG;
+    if (N <= 0 || T <= 0 || HK <= 0 || HV <= 0 || HV % HK || (dv != 64 && dv != 128)) return GDN_ERR_INVALID_ARG;
+    if ((int64_t)N * T > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+    gdn::SsmArgs s{};
+    s.x = x;
+    s.b = b;
+    s.c = c;
+    s.dt = dt;
+    s.a = a;
+    s.N = N;
+    s.T = T;
+    s.HK = HK;
+    s.HV = HV;
+    s.dk = 128;
+    s.dv = dv;
+    s.x_row = (int64_t)HV * dv;
+    s.b_row = s.c_row = (int64_t)HK * 128;
+    s.dtype = GDN_BF16;
+    s.softplus = true;
+    s.y = y;
+    s.hT = hT;
+    s.workspace = workspace;
+    s.workspace_bytes = workspace_bytes;
+    s.timeout_test = true;
+    if (workspace_bytes < gdn::ssm_workspace_bytes(s)) return GDN_ERR_WORKSPACE;
+    const cudaError_t err = gdn::launch_ssm_prefill(s, reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}

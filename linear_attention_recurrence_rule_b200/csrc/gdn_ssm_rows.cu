@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(128, ROWS == 8 ? 4 : ROWS == 4 ? 7 : 8)
 scan_rows_kernel(const RowParams p) {
     constexpr int LPR = DK / kCols;          // lanes per row group
     constexpr int RPW = rows_per_warp<DK, ROWS>();
+    constexpr int AT_ONCE = ROWS == 2 ? 4 : 2;   // tokens whose sums are reduced together
     constexpr int V = 16 / (int)sizeof(T);   // elements per 16 bytes
     extern __shared__ __align__(16) uint8_t raw[];
     Tile<DK, T> *tiles = reinterpret_cast<Tile<DK, T> *>(raw);
@@ -272,8 +273,9 @@ scan_rows_kernel(const RowParams p) {
         auto tile = [&](auto kind) {
             int i = 0;
 #pragma unroll 1
-            for (; i + 2 <= m; i += 2) tokens(std::integral_constant<int, 2>{}, kind, i);
-            if (i < m) tokens(std::integral_constant<int, 1>{}, kind, i);
+            for (; i + AT_ONCE <= m; i += AT_ONCE) tokens(std::integral_constant<int, AT_ONCE>{}, kind, i);
+#pragma unroll 1
+            for (; i < m; ++i) tokens(std::integral_constant<int, 1>{}, kind, i);
         };
         const float total = t.total;
         if (total > 0.f) {

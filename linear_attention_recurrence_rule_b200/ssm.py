@@ -22,7 +22,10 @@ def _code(t, name):
 
 
 def _check(t, name, shape, dtype, dev, strided=False):
-    """A CUDA tensor of this shape, dtype and device, contiguous unless `strided`."""
+    """Address of a CUDA tensor of this shape, dtype and device, contiguous unless `strided`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev.index and t.dtype is dtype and \
+            t.shape == shape and (strided or t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
@@ -31,9 +34,7 @@ def _check(t, name, shape, dtype, dev, strided=False):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not strided and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _opt(t, name, shape, dtype, dev):

@@ -212,6 +212,34 @@ def test_two_captured_graphs_with_their_own_workspaces():
         assert gdn.gdn_read_status(s[-1]) == 0
 
 
+@pytest.mark.parametrize("HK,HV,dv", [(1, 2, 128), (1, 2, 64), (1, 3, 64)])
+def test_timeout_path_then_normal_call(HK, HV, dv):
+    """Waits that give up (no hang: the test-only call has one role stopped from the start,
+    and the flag set that the others' waits look at) leave the status word, free everything
+    and return; the next call is exact again."""
+    import ctypes
+    from linear_attention_recurrence_rule_b200 import gdn as binding
+    P, i32 = ctypes.c_void_p, ctypes.c_int
+    f = binding.load_library().gdn_selftest_ssm_timeout
+    f.restype, f.argtypes = i32, [P] * 5 + [i32, ctypes.c_int64, i32, i32, i32, P, P, P, ctypes.c_size_t, P]
+    T = 1500
+    p = make_scan([T], HK, HV, 128, dv, BF16, seed=41, packed=False, h0=False)
+    p["d"] = p["dt_bias"] = None
+    g = to_cuda(p)
+    x, b, c = (t.contiguous() for t in split_row(g["row"], HK, HV, 128, dv))
+    n = gdn.gdn_ssm_prefill_workspace_size(1, T, HK, HV, 128, dv, BF16, False)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    y, hT = torch.empty_like(x), torch.empty(1, HV, dv, 128, device="cuda")
+    rc = f(*(t.data_ptr() for t in (x, b, c, g["dt"], g["a"])), 1, T, HK, HV, dv, y.data_ptr(), hT.data_ptr(),
+           ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert gdn.gdn_read_status(ws) == binding.GDN_ERR_TIMEOUT
+    y, hT = gdn.gdn_ssm_prefill(x, b, c, g["dt"], g["a"], softplus=True, workspace=ws)
+    assert gdn.gdn_read_status(ws) == 0
+    check_scan(y, hT, oracle(p, HK, HV, 128, dv, True), BF16, True)
+
+
 # ---------------------------------------------------------------- one token
 def make_step(N, HK, HV, dk, dv, W, dtype, seed, row_extra=0):
     gen = torch.Generator().manual_seed(seed)
