@@ -171,6 +171,13 @@ scan_rows_kernel(const RowParams p) {
         }
 
     const int ntiles = (seg.len + kTile - 1) / kTile;
+    // dt of the tile that is issued next (warp 0): loaded a tile ahead, so that its trip
+    // to memory does not stand between a tile and the one before it
+    auto load_dt = [&](int k) {
+        const int64_t t = (int64_t)k * kTile + lane;
+        return warp == 0 && lane < kTile && t < seg.len ? dtp[t * p.HV] : 0.f;
+    };
+    float ahead = load_dt(0);
     auto issue = [&](int k) {
         if (k < ntiles) {
             Tile<DK, T> &t = tiles[k & 1];
@@ -188,7 +195,8 @@ scan_rows_kernel(const RowParams p) {
             }
             if (warp == 0) {
                 const bool in = lane < m;
-                const float dl = in ? step_size(dtp[(at + lane) * p.HV], bias, p.softplus) : 0.f;
+                const float dl = in ? step_size(ahead, bias, p.softplus) : 0.f;
+                ahead = load_dt(k + 1);
                 const float al = in ? expf(dl * ah) : 1.f;
                 float gamma = al;
 #pragma unroll
