@@ -565,9 +565,14 @@ GDN_API gdn_status gdn_chunk_prefill_layer(const void *q, const void *k, const v
  * Supported: HV % HK == 0; dk, dv in {32, 64, 128}; GDN_BF16 or GDN_F32; fewer than
  * 2^31 tokens.  States are fp32 throughout.  Alignment: x, b, c, y, h0, hT, workspace
  * 16 bytes, the rows' byte strides multiples of 16.
+ * No output may overlap an input or another output (but hT may be h0).
  * workspace: device scratch of gdn_ssm_prefill_workspace_size(...) bytes (may be NULL
  * where that is 0), not to be shared by calls that may overlap; gdn_read_status as
- * after gdn_chunk_prefill (where the size is not 0).
+ * after gdn_chunk_prefill (where the size is not 0).  It holds a state per segment: long
+ * sequences are cut until the SMs are filled, packed ones at most into T / segment + N.
+ * bf16 with dk = 128 and dv 64 or 128 runs on the tensor cores (y: every term rounded to
+ * bf16 once or twice on the way, about 2^-8 of its size in all; hT: fp32 accuracy),
+ * everything else on the CUDA cores in fp32.  Up to five launches on `stream`.
  * N == 0: GDN_OK, nothing launched.  T == 0: hT gets h0 (or zero).
  */
 GDN_API gdn_status gdn_ssm_prefill(const void *x, const void *b, const void *c, const float *dt,
@@ -592,8 +597,8 @@ GDN_API size_t gdn_ssm_prefill_workspace_size(int N, int64_t T, int HK, int HV, 
  *   already convolved and the other conv arguments are ignored.
  *   dt [N][HV] fp32; a, d, dt_bias as above; state, state_out [N][HV][dv][dk] fp32
  *   (the same buffer: in place; otherwise they must not overlap); y [N][HV][dv] dtype
- * flags: GDN_SSM_SOFTPLUS, GDN_CONV_SILU.  Supported: dk in {32, 64, 128},
- * 1 <= dv <= 256, widths as gdn_short_conv, N <= 262140.  Alignment: states and
+ * y must not overlap anything else.  flags: GDN_SSM_SOFTPLUS, GDN_CONV_SILU.
+ * Supported: dk in {32, 64, 128}, 1 <= dv <= 256, widths as gdn_short_conv, N <= 262140.  Alignment: states and
  * workspace 16 bytes, the rest their element's size.  workspace: device scratch of
  * gdn_ssm_step_workspace_size(...) bytes (the convolved row in fp32), not to be shared
  * by calls that may overlap.  Two launches, the second one dependent on the first.

@@ -14,7 +14,7 @@
 //    the whole segment with the decays to the segment's END in w_j (all <= delta_j, so
 //    nothing overflows and nothing is rescaled on the way) -- one product with the
 //    tokens as its inner dimension, chunk by chunk from the end.  w_j x_j is a full
-//    fp32 value, so it enters as three bf16 terms (2^-24): the states returned to the
+//    fp32 value, so it enters as three bf16 terms (exactly): the states returned to the
 //    caller carry fp32 accuracy.
 //  * combine_kernel (gdn_ssm_rows.cu): chains the segments in place; hT.
 //  * scan_kernel, one CTA per (segment, value tile), chunk by chunk: C B^T, the masked
@@ -25,19 +25,29 @@
 //
 // A value tile is 128 columns where it can be: one head of 128, or two heads of 64 of
 // one group, which share C B^T and the loads of b and c; else one head of 64.
-// The state is kept transposed, S^T [dk lanes][value columns].
 //
-// scan_kernel's warps: loader (TMA), MMA issuer, table (step sizes, running sums, the
-// factors below), and by groups of 4 warps -- mask (C B^T -> P in the same tensor memory
-// columns), state (S -> bf16 operand, S times e^{G_L}), weight (w x, in pieces of 32
-// tokens through a ring of 3) and output
-// (two groups, half of the columns each).  The mask takes e^{G_i-G_j} as the decays
-// behind j in its 32-token block times those from there to i, both <= 1: one
+// scan_kernel keeps its state transposed, S^T [dk lanes][value columns].  Its warps: a
+// loader (TMA), the MMA issuer, two for the tables (step sizes, running sums, the factors
+// below; every other chunk each), and groups of four -- mask (C B^T -> P in the same
+// tensor memory columns), state (S -> bf16 operand, S times e^{G_L}), weight (w x, in
+// pieces of 32 tokens through a ring of 3) and output.  The mask takes e^{G_i-G_j} as the
+// decays behind j in its 32-token block times those from there to i, both <= 1: one
 // exponential per row and block (the diagonal blocks one per element where their decays
-// are too strong for a common reference).  All
-// sums of log decays run over the tokens between the two ends (block sums), none is a
-// difference of running sums: a token that forgets everything (a log decay of
-// thousands) would leave such differences few digits for the tokens behind it.
+// are too strong for a common reference).  All sums of log decays run over the tokens
+// between the two ends (block sums), none is a difference of running sums: a token that
+// forgets everything (a log decay of thousands) would leave such differences few digits
+// for the tokens behind it.
+//
+// What bounds it (64K tokens, 32 heads of 128, 16 groups: 1.62 GB, 247 us at the measured
+// copy rate; 720 us in a long run, under the 1000 W cap at 1.68 GHz, 640 us in a short
+// one): scan_kernel 410 us, states_kernel 214 us, combine_kernel 21 us.  In scan_kernel it
+// is shared memory: per 128 tokens and tile the tensor cores read 224 KB (1792 cycles at
+// 128 bytes a cycle), TMA writes 96 KB (768) and the warps move about 280 KB (2240), of
+// 5600 cycles measured; the roles' instructions (2400 issue slots per scheduler) come
+// next.  Measured and not kept: eight weight warps (640 -> 665 us), eight output warps
+// (683 -> 700 us), a skip term from L2 instead of the shared x tile (740 -> 790 us), roles
+// unrolled in full (they miss the instruction cache: 740 us -> 410 us rolled), MMAs issued
+// in rolled loops (95-130 cycles each instead of 64).
 //
 // Waits are bounded (about 2 s): a wait that gives up records GDN_ERR_TIMEOUT in the
 // workspace's first word and every role winds down.
@@ -209,8 +219,10 @@ __device__ __forceinline__ float block_sums(float g, int lane, float &pre, float
 // shared memory with transposing matrix loads, weight it and put it into tensor memory as
 // three bf16 terms (the A operand, lanes = value columns): the products then read only b
 // from shared memory, whose bandwidth is what bounds this kernel (with the terms in
-// shared memory it moved 384 KB per 128 tokens of a 128-wide tile instead of 176 KB, and
-// took 280 us instead of XXX us for 64K tokens of 32 heads of 128).  The first terms and
+// shared memory it moved 384 KB per 128 tokens of a 128-wide tile instead of 192 KB, and
+// took 280 us instead of 214 us for 64K tokens of 32 heads of 128).  Its 24 products a
+// chunk take 1540 cycles, the workers' chain of a piece (load, split, store, signal) about
+// as long again.  The first terms and
 // the two small ones have an accumulator each, so that the small ones are not rounded
 // away against the large sum, and every kFlush chunks both are added to sums in the
 // workers' registers: the tensor cores truncate, and over the 456 additions of a 7K-token
