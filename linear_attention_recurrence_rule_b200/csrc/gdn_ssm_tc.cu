@@ -345,27 +345,28 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         for (int j = issued > 3 ? issued - 3 : 0; j < issued; ++j) wt.drain(SB_F0 + j % 3, (uint32_t)((j / 3) & 1));
     } else if (warp == 1) {
         const uint32_t id = idesc_bf16(128, DK, false, true);
+        const bool issuer = elect_one();
+        int r = 0, ph = 0;           // ring slot of the next piece and its phase
         for (int j = 0; j < nch && ok; ++j) {
             const bool fresh = j % kFlush == 0;
             if (fresh && j > 0) ok = wt(SB_READ, (uint32_t)((j / kFlush - 1) & 1));
             ok = ok && stage_full(j);
             const uint64_t b0 = sdesc_sw128(sb + (j % 3) * Cfg::STAGE, 16384, 1024);
-#pragma unroll 1
-            for (int q = 0; q < 4 && ok; ++q) {
-                const int pc = 4 * j + q, r = pc % kPieces;
-                ok = wt(SB_WF0 + r, (uint32_t)((pc / kPieces) & 1));
+            // (unrolled: the tensor cores hold only a few products ahead of the one that runs)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                ok = ok && wt(SB_WF0 + r, (uint32_t)ph);
                 if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint64_t bd = desc_add(b0, q * 4096 + k * 2048);
-                        const uint32_t a = tmem + TS_A + r * TS_PIECE + 8 * k;
-                        const uint32_t add = !fresh || q + k > 0;
-                        mma_bf16_ts(tmem + TS_D, a, bd, id, add);
-                        mma_bf16_ts(tmem + TS_DS, a + 16, bd, id, add);
-                        mma_bf16_ts(tmem + TS_DS, a + 32, bd, id, 1);
-                    }
+                if (issuer) {
+                    const uint32_t a = tmem + TS_A + r * TS_PIECE;
+                    const uint32_t add = !fresh || q > 0;
+                    mma_bf16_ts(tmem + TS_D, a, desc_add(b0, q * 4096), id, add);
+                    mma_bf16_ts(tmem + TS_DS, a + 16, desc_add(b0, q * 4096), id, add);
+                    mma_bf16_ts(tmem + TS_DS, a + 32, desc_add(b0, q * 4096), id, 1);
+                    mma_bf16_ts(tmem + TS_D, a + 8, desc_add(b0, q * 4096 + 2048), id, 1);
+                    mma_bf16_ts(tmem + TS_DS, a + 24, desc_add(b0, q * 4096 + 2048), id, 1);
+                    mma_bf16_ts(tmem + TS_DS, a + 40, desc_add(b0, q * 4096 + 2048), id, 1);
                     mma_commit(&bars[SB_WE0 + r]);
                     if (q == 3) {
                         mma_commit(&bars[SB_E0 + j % 3]);
@@ -373,6 +374,10 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                     }
                 }
                 __syncwarp();
+                if (++r == kPieces) {
+                    r = 0;
+                    ph ^= 1;
+                }
             }
         }
         // every product issued here has completed before tensor memory is released

@@ -118,3 +118,17 @@ def test_residual_norm_optional_parts_streams_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(h, wh) and torch.equal(n, gdn.gdn_gated_norm(want, x))
     assert gdn.gdn_residual_norm(x[:0])[0].shape == (0, 9, 256)
+
+
+def test_offsets_past_32_bits():
+    rows, C = 530_000, 4096                                   # 2.2e9 elements
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty(rows, C, dtype=BF16, device="cuda").normal_(generator=gen)
+    w = torch.empty(128, device="cuda").normal_(generator=gen)
+    assert x.numel() > 2 ** 31
+    y = gdn.gdn_gated_norm(x.view(rows, 32, 128), x.view(rows, 32, 128), w)
+    assert torch.equal(y[-5:], gdn.gdn_gated_norm(x[-5:].view(5, 32, 128), x[-5:].view(5, 32, 128), w))
+    del y
+    y, h = gdn.gdn_residual_norm(x, x, scale=0.5)
+    y2, h2 = gdn.gdn_residual_norm(x[-5:], x[-5:], scale=0.5)
+    assert torch.equal(y[-5:], y2) and torch.equal(h[-5:], h2)

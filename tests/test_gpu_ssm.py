@@ -407,3 +407,43 @@ def test_block_over_prompt_then_tokens(dtype, dk, dv):
         within(y, S.f64(yf)[0, rows], lim, "token y")
         assert bool(torch.isfinite(out).all())
     assert torch.equal(conv, convf)
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+def test_prefill_offsets_past_32_bits():
+    # 2.2e9 elements of x and y: the last heads of the last tokens against a call on those
+    # heads alone (other cuts, so within the bounds of two results: the output's rounding
+    # each, and twice the terms' -- taken relative to the rows' norms)
+    HK, HV, dk, dv, T = 1, 64, 128, 128, 270_000
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.empty(1, T, HV, dv, dtype=BF16, device="cuda").normal_(generator=gen)
+    b, c = (torch.empty(1, T, HK, dk, dtype=BF16, device="cuda").normal_(generator=gen) for _ in range(2))
+    dt = torch.empty(1, T, HV, device="cuda").normal_(generator=gen)
+    a, bias = -torch.linspace(0.5, 4, HV, device="cuda"), torch.full((HV,), -2.0, device="cuda")
+    y, hT = gdn.gdn_ssm_prefill(x, b, c, dt, a, dt_bias=bias, softplus=True)
+    assert y.numel() > 2 ** 31
+    few = slice(HV - 2, HV)
+    y2, h2 = gdn.gdn_ssm_prefill(x[:, :, few], b, c, dt[:, :, few].contiguous(), a[few].contiguous(),
+                                 dt_bias=bias[few].contiguous(), softplus=True)
+    u, v = y[0, -4096:, few].double(), y2[0, -4096:].double()
+    assert float((u - v).norm() / v.norm()) < 6 * U[BF16]
+    assert float((hT[:, few] - h2).double().norm() / h2.double().norm()) < 2e-6
+    # and of the first tokens, so that no offset wraps onto them
+    u, v = y[0, :4096, few].double(), y2[0, :4096].double()
+    assert float((u - v).norm() / v.norm()) < 6 * U[BF16]
+
+
+def test_step_offsets_past_32_bits():
+    N, HK, HV, dk, dv, W = 4200, 1, 32, 128, 128, 4          # 2.2e9 state elements
+    C = HV * dv + 2 * HK * dk
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.empty(*s, device="cuda").normal_(generator=gen)   # noqa: E731
+    state, xbc, dt = r(N, HV, dv, dk), r(N, C).to(BF16), r(N, HV)
+    assert state.numel() > 2 ** 31
+    cw, cs, a = r(C, W), r(N, W - 1, C).to(BF16), -torch.rand(HV, generator=gen, device="cuda")
+    last = slice(N - 3, N)
+    s2, c2 = state[last].clone(), cs[last].clone()
+    y2 = gdn.gdn_ssm_step(xbc[last].contiguous(), dt[last].contiguous(), a, s2, conv_weight=cw, conv_state=c2, silu=True,
+                          softplus=True)
+    y = gdn.gdn_ssm_step(xbc, dt, a, state, conv_weight=cw, conv_state=cs, silu=True, softplus=True)
+    assert torch.equal(y[last], y2) and torch.equal(state[last], s2) and torch.equal(cs[last], c2)
