@@ -19,9 +19,10 @@
 //  * combine_kernel (gdn_ssm_rows.cu): chains the segments in place; hT.
 //  * scan_kernel, one CTA per (segment, value tile), chunk by chunk: C B^T, the masked
 //    and decayed P, C S^T, P X and the next state, all on tcgen05 with the state in
-//    tensor memory.  Its state only feeds the bf16 y: w_j x_j, S and P enter as one
-//    bf16 operand each, so a term of y inside its chunk is rounded once on the way and
-//    one from before it twice.
+//    tensor memory.  Its state only feeds the bf16 y: w_j, w_j x_j, S and P are rounded
+//    to bf16, so a term of y inside its chunk is rounded once on the way and one from
+//    before it three times (w_j in bf16 makes the weighting one packed multiply: the
+//    scan's instructions bound it as much as anything, see below).
 //
 // A value tile is 128 columns where it can be: one head of 128, or two heads of 64 of
 // one group, which share C B^T and the loads of b and c; else one head of 64.
@@ -78,7 +79,6 @@ struct TcParams {
     unsigned int *status;
     bool chained;       // scan: start states from the slots (otherwise h0)
     bool whole;         // states: the last segment's state is wanted too
-    bool wide_store;    // y is 32-byte aligned
     int timeout_test;   // 1 (test only): the MMA warp issues nothing, as if its first wait had given up
     SegMap map;
 };
@@ -117,6 +117,13 @@ __device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap *map, int x
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(x), "r"(y)
+                 : "memory");
+}
+// 2-D tiled store from shared memory, tracked by the issuing thread's bulk group
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y)
                  : "memory");
 }
 __device__ __forceinline__ void arrive(uint64_t *bar) {
@@ -186,6 +193,11 @@ __device__ __forceinline__ float2 subp(float2 a, float2 b) {
     memcpy(&d, &ud, 8);
     return d;
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, __nv_bfloat162 w) {
+    const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), w);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
 // One head's decay and step bias, a * log2 e and dt_bias.
 struct HeadTab {
     float ah, bias;
@@ -565,7 +577,7 @@ constexpr uint32_t T_CB = 0, T_Y1 = 128, T_Y2 = 256, T_S = 384;
 template <int VT, int NH>
 __global__ void __launch_bounds__(kScThreads, 1)
 scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
-            const __grid_constant__ CUtensorMap tm_c, const TcParams p) {
+            const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y, const TcParams p) {
     using Cfg = ScanCfg<VT, NH>;
     constexpr int DV = VT / NH;
     extern __shared__ uint8_t raw[];
@@ -948,16 +960,9 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint4 u = lds128(src + v * 16384 + half * 2048);
-                        const float w = tab[16 * half] * behind;
-                        const float2 w2 = make_float2(w, w);
-                        const uint32_t xs[4] = {u.x, u.y, u.z, u.w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = mulp(unpack2(xs[i]), w2);
-                            o[i] = pack_bf16x2(f.x, f.y);
-                        }
-                        sts128(dst + v * 4096 + half * 2048, o[0], o[1], o[2], o[3]);
+                        const __nv_bfloat162 w = __float2bfloat162_rn(tab[16 * half] * behind);
+                        sts128(dst + v * 4096 + half * 2048, mul_bf16x2(u.x, w), mul_bf16x2(u.y, w), mul_bf16x2(u.z, w),
+                               mul_bf16x2(u.w, w));
                     }
                 }
                 fence_proxy_async_smem();
@@ -1007,7 +1012,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
             ok = wt(B_Y, (uint32_t)(c & 1));
             if (!ok) break;
             tc_fence_after();
-            const bool in = c < last || i < tail;
+            const bool whole = c < last || tail == L;
             const uint32_t xtile = sb + Cfg::O_X + (c & 1) * Cfg::XT;
 #pragma unroll 1
             for (int g = 0; g < VT / 16; ++g) {
@@ -1029,19 +1034,31 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                     f = fma2(de2, unpack2(xw[u]), f);
                     o[u] = pack_bf16x2(f.x, f.y);
                 }
-                if (in) {
-                    if (p.wide_store) {
-                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(yr + 16 * g), "r"(o[0]),
-                                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                     : "memory");
-                    } else {
-                        reinterpret_cast<uint4 *>(yr + 16 * g)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                        reinterpret_cast<uint4 *>(yr + 16 * g)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
+                if (whole) {
+                    // y takes x's place in the tile (the weights and P X are done with it)
+                    sts128(xa + sw128_chunk(i, ch), o[0], o[1], o[2], o[3]);
+                    sts128(xa + sw128_chunk(i, ch + 1), o[4], o[5], o[6], o[7]);
+                } else if (i < tail) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(yr + 16 * g);
+                    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
                 }
             }
             tc_fence_before();
             warp_arrive(&bars[B_YE]);
+            if (whole) {
+                // this warp's 32 rows, by the copy engine
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll
+                    for (int q = 0; q < VT / 64; ++q)
+                        tma_store_2d(&tm_y, xtile + q * 16384 + quad * 4096, head * DV + 64 * q,
+                                     (int)(seg.t0 + (int64_t)c * L) + 32 * quad);
+                    bulk_commit_group();
+                    bulk_wait_group_read0();
+                }
+            }
             warp_arrive(&bars[B_XE0 + (c & 1)]);
             yr += (size_t)L * p.HV * DV;
         }
@@ -1119,7 +1136,7 @@ cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
                static_cast<__nv_bfloat16 *>(a.y),
                reinterpret_cast<float *>(ws + cut.state), reinterpret_cast<float *>(ws + cut.decay),
                reinterpret_cast<unsigned int *>(ws), states, a.hT != nullptr,
-               (reinterpret_cast<uintptr_t>(a.y) & 31u) == 0, a.timeout_test,
+               a.timeout_test,
                SegMap{nullptr, nullptr, a.N, cut.nseg, a.T, cut.seg_len}};
     if (packed) {
         p.map.table = reinterpret_cast<int4 *>(ws + cut.table);
@@ -1129,13 +1146,14 @@ cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
     }
     const uint64_t tokens = (uint64_t)(packed ? a.T : (int64_t)a.N * a.T);
-    CUtensorMap tx{}, tb{}, tcm{};
+    CUtensorMap tx{}, tb{}, tcm{}, ty{};
     if (tokens > 0) {
-        const uint32_t box[2] = {64, (uint32_t)L};
+        const uint32_t box[2] = {64, (uint32_t)L}, ybox[2] = {64, 32};
         const uint64_t dx[2] = {(uint64_t)a.HV * a.dv, tokens}, db[2] = {(uint64_t)a.HK * DK, tokens};
-        const uint64_t sx[1] = {(uint64_t)a.x_row * 2}, sbb[1] = {(uint64_t)a.b_row * 2}, sc[1] = {(uint64_t)a.c_row * 2};
+        const uint64_t sx[1] = {(uint64_t)a.x_row * 2}, sbb[1] = {(uint64_t)a.b_row * 2}, sc[1] = {(uint64_t)a.c_row * 2},
+                       sy[1] = {(uint64_t)a.HV * a.dv * 2};
         if (!encode_bf16_map(&tx, a.x, 2, dx, sx, box) || !encode_bf16_map(&tb, a.b, 2, db, sbb, box) ||
-            !encode_bf16_map(&tcm, a.c, 2, db, sc, box))
+            !encode_bf16_map(&tcm, a.c, 2, db, sc, box) || !encode_bf16_map(&ty, a.y, 2, dx, sy, ybox))
             return cudaErrorInvalidValue;
     }
     if (states) {
@@ -1151,8 +1169,8 @@ cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
         err = cudaFuncSetAttribute(scan_kernel<VT, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (err != cudaSuccess) return err;
         if (states)
-            return launch_after(scan_kernel<VT, NH>, dim3((unsigned)grid), dim3(kScThreads), bytes, stream, tx, tb, tcm, p);
-        scan_kernel<VT, NH><<<(unsigned)grid, kScThreads, bytes, stream>>>(tx, tb, tcm, p);
+            return launch_after(scan_kernel<VT, NH>, dim3((unsigned)grid), dim3(kScThreads), bytes, stream, tx, tb, tcm, ty, p);
+        scan_kernel<VT, NH><<<(unsigned)grid, kScThreads, bytes, stream>>>(tx, tb, tcm, ty, p);
     }
     return cudaGetLastError();
 }
