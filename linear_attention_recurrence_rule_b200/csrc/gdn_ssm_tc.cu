@@ -660,6 +660,15 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                 tma_load_2d(sm + Cfg::O_B + s * 32768 + 16384, &tm_b, &bars[B_BF0 + s], gb + 64, t);
             }
             nb = c + 1;
+            // (c before x: the one C tile's load is what the next scores wait for)
+            if (c >= 1) ok = wt(B_CE, (uint32_t)((c - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[B_CF], 32768);
+                tma_load_2d(sm + Cfg::O_C, &tm_c, &bars[B_CF], gb, t);
+                tma_load_2d(sm + Cfg::O_C + 16384, &tm_c, &bars[B_CF], gb + 64, t);
+            }
+            nc = c + 1;
             if (c >= 2) ok = wt(B_XE0 + s, par2_before(c));
             if (!ok) break;
             if (lane == 0) {
@@ -669,14 +678,6 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                     tma_load_2d(sm + Cfg::O_X + s * Cfg::XT + q * 16384, &tm_x, &bars[B_XF0 + s], head * DV + 64 * q, t);
             }
             nx = c + 1;
-            if (c >= 1) ok = wt(B_CE, (uint32_t)((c - 1) & 1));
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars[B_CF], 32768);
-                tma_load_2d(sm + Cfg::O_C, &tm_c, &bars[B_CF], gb, t);
-                tma_load_2d(sm + Cfg::O_C + 16384, &tm_c, &bars[B_CF], gb + 64, t);
-            }
-            nc = c + 1;
             __syncwarp();
         }
         // no load stays in flight behind this CTA, whatever the other roles do
