@@ -570,8 +570,9 @@ GDN_API gdn_status gdn_chunk_prefill_layer(const void *q, const void *k, const v
  * where that is 0), not to be shared by calls that may overlap; gdn_read_status as
  * after gdn_chunk_prefill (where the size is not 0).  It holds a state per segment: long
  * sequences are cut until the SMs are filled, packed ones at most into T / segment + N.
- * bf16 with dk = 128 and dv 64 or 128 runs on the tensor cores (y: every term rounded to
- * bf16 once or twice on the way, about 2^-8 of its size in all; hT: fp32 accuracy),
+ * bf16 with dk = 128 and dv 64 or 128 runs on the tensor cores (y: a term is rounded to
+ * bf16 once on the way, one from an earlier chunk of 128 tokens three times, by at most
+ * 2^-8 of its size each; hT: fp32 accuracy),
  * everything else on the CUDA cores in fp32.  Up to five launches on `stream`.
  * N == 0: GDN_OK, nothing launched.  T == 0: hT gets h0 (or zero).
  */

@@ -21,8 +21,7 @@
 //    and decayed P, C S^T, P X and the next state, all on tcgen05 with the state in
 //    tensor memory.  Its state only feeds the bf16 y: w_j, w_j x_j, S and P are rounded
 //    to bf16, so a term of y inside its chunk is rounded once on the way and one from
-//    before it three times (w_j in bf16 makes the weighting one packed multiply: the
-//    scan's instructions bound it as much as anything, see below).
+//    before it three times (w_j in bf16 makes the weighting one packed multiply).
 //
 // A value tile is 128 columns where it can be: one head of 128, or two heads of 64 of
 // one group, which share C B^T and the loads of b and c; else one head of 64.
@@ -39,16 +38,25 @@
 // forgets everything (a log decay of thousands) would leave such differences few digits
 // for the tokens behind it.
 //
+// y leaves through the x tile: the output warps put their rows over the x they have read
+// and TMA stores the tile (a part chunk is stored by the warps).  Their own stores, 32
+// bytes a lane and a row apart, cost 15 to 80 us of the 64K case's 640 (the more, the
+// lower the clock).
+//
 // What bounds it (64K tokens, 32 heads of 128, 16 groups: 1.62 GB, 247 us at the measured
-// copy rate; 720 us in a long run, under the 1000 W cap at 1.68 GHz, 640 us in a short
-// one): scan_kernel 410 us, states_kernel 214 us, combine_kernel 21 us.  In scan_kernel it
-// is shared memory: per 128 tokens and tile the tensor cores read 224 KB (1792 cycles at
-// 128 bytes a cycle), TMA writes 96 KB (768) and the warps move about 280 KB (2240), of
-// 5600 cycles measured; the roles' instructions (2400 issue slots per scheduler) come
-// next.  Measured and not kept: eight weight warps (640 -> 665 us), eight output warps
-// (683 -> 700 us), a skip term from L2 instead of the shared x tile (740 -> 790 us), roles
-// unrolled in full (they miss the instruction cache: 740 us -> 410 us rolled), MMAs issued
-// in rolled loops (95-130 cycles each instead of 64).
+// copy rate; 670 us in a long run, under the 1000 W cap, 570 to 620 us in a short one):
+// scan_kernel 358 us, states_kernel 203 us, combine_kernel 21 us.  scan_kernel takes about
+// 5000 cycles per 128 tokens, and no one pipe fills them: the tensor cores read 224 KB of
+// shared memory (1792 cycles at 128 bytes a cycle) and the schedulers issue 2400
+// instructions each; taking any one role's shared memory accesses out changed the time by
+// 5% at most, 13% fewer instructions by 0.5%.  What is left is the chain of one chunk:
+// C S^T, the load of c into its one tile, C B^T, the mask, P X, the read-out, and beside it
+// the state's way through the state warps and back.  A second c tile would shorten it; the
+// tiles of b, c, x and P fill the 227 KB.  Measured and not kept: eight weight warps (640 ->
+// 665 us), eight output or state warps (683 -> 700 us), a skip term from L2 instead of the
+// shared x tile (740 -> 790 us), C S^T issued at whichever is ready first (565 -> 585 us),
+// roles unrolled in full (they miss the instruction cache: 740 us against 410 us rolled),
+// MMAs issued in rolled loops (95-130 cycles each instead of 64).
 //
 // Waits are bounded (about 2 s): a wait that gives up records GDN_ERR_TIMEOUT in the
 // workspace's first word and every role winds down.
