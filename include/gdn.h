@@ -563,7 +563,7 @@ GDN_API gdn_status gdn_chunk_prefill_layer(const void *q, const void *k, const v
  * token's, so that the three may be parts of one wider row (the convolved x | b | c
  * row of gdn_short_conv); 0: dense.  y is dense.
  * Supported: HV % HK == 0; dk, dv in {32, 64, 128}; GDN_BF16 or GDN_F32; fewer than
- * 2^31 tokens.  States are fp32 throughout.  Alignment: x, b, c, y, h0, hT, workspace
+ * 2^31 tokens, N * HV < 2^28.  States are fp32 throughout.  Alignment: x, b, c, y, h0, hT, workspace
  * 16 bytes, the rows' byte strides multiples of 16.
  * No output may overlap an input or another output (but hT may be h0).
  * workspace: device scratch of gdn_ssm_prefill_workspace_size(...) bytes (may be NULL

@@ -20,6 +20,8 @@ gdn_status check_ssm_sizes(int N, int64_t T, int HK, int HV, int dk, int dv, gdn
     if (!known(dtype)) return GDN_ERR_INVALID_ARG;
     if (!gdn::ssm_supported(dk, dv)) return GDN_ERR_UNSUPPORTED;
     if ((int64_t)HV * dv > kGrid || (int64_t)HK * dk > kGrid) return GDN_ERR_UNSUPPORTED;
+    // grid.x: up to 4 CTAs for each segment's state; cutting adds some hundred states at most
+    if ((int64_t)N * HV > kGrid / 8) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

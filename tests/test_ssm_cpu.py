@@ -41,6 +41,8 @@ def test_prefill_refusals(lib):
     assert prefill(lib, dv=256) == UNSUPPORTED
     assert prefill(lib, N=1 << 20, T=1 << 20) == UNSUPPORTED
     assert prefill(lib, N=2, T=(1 << 62) + 1) == UNSUPPORTED
+    assert prefill(lib, N=1 << 27, T=1, HV=2) == UNSUPPORTED    # 2^28 states
+    assert prefill(lib, N=1 << 27, T=1, HV=2, dtype=gdn.GDN_F32, dk=32, dv=32) == UNSUPPORTED
     assert prefill(lib, xr=120) == INVALID          # rows would overlap
     assert prefill(lib, br=64) == INVALID
     for name in ("x", "b", "c", "y", "h0", "hT"):
