@@ -17,7 +17,10 @@ struct SegMap {
     int N, nseg;            // sequences; segments per sequence (without the table)
     int64_t T;              // tokens per sequence (without the table)
     int seg_len;
+    const int *order;       // [bound] which segment a CTA takes, the longest first, or null: in their order
 };
+// A table of more segments than this stays in its order: the work then evens out by itself.
+constexpr int kOrdered = 1024;
 
 struct Seg {
     int n, idx, len;        // sequence, index in it, tokens
@@ -25,9 +28,11 @@ struct Seg {
     bool ok, last;
 };
 
-__device__ __forceinline__ Seg find_seg(const SegMap &m, int s) {
+// segment of the s-th CTA (of each head's); s becomes the segment's number
+__device__ __forceinline__ Seg find_seg(const SegMap &m, int &s) {
     Seg r;
     if (m.table) {
+        if (m.order) s = m.order[s];
         r.ok = s < m.first[m.N];
         if (!r.ok) return r;
         const int4 e = m.table[s];
@@ -50,7 +55,8 @@ __device__ __forceinline__ Seg find_seg(const SegMap &m, int s) {
 }
 
 // Segment table of a packed batch; the chaining of the segments (gdn_ssm_rows.cu).
-cudaError_t launch_plan(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first, cudaStream_t stream);
+cudaError_t launch_plan(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first, int *order,
+                        cudaStream_t stream);
 cudaError_t launch_combine(float *seg_state, const float *seg_decay, const float *h0, float *hT, int N, int HV, int elems,
                            bool whole, const SegMap &map, cudaStream_t stream);
 // the tensor-core scan (gdn_ssm_tc.cu)

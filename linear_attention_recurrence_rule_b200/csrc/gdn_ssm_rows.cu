@@ -138,7 +138,8 @@ scan_rows_kernel(const RowParams p) {
     const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rpc = (nt >> 5) * RPW;         // rows per CTA
     const int bands = p.dv / rpc;
-    const int slot = blockIdx.x / (p.HV * bands), hb = blockIdx.x - slot * (p.HV * bands);
+    int slot = blockIdx.x / (p.HV * bands);
+    const int hb = blockIdx.x - slot * (p.HV * bands);
     if (READ) wait_for_previous();
     else let_next_start();
     const Seg seg = find_seg(p.map, slot);
@@ -363,8 +364,12 @@ combine_kernel(float *seg_state, const float *seg_decay, const float *h0, float 
 }
 
 // Segment table of a packed batch: one block, a running sum over tiles of 1024 sequences.
+// With `order` also the segments by falling length (each counts those before it): CTAs
+// take their work in the order of their indexes, and a long segment that starts behind
+// short ones is waited for by all (8 prompts of 0 to 12288 tokens, 32 heads of 64: the
+// schedule 40 -> 32 chunks long, the call 246 -> 200 to 208 us).
 __global__ void __launch_bounds__(1024)
-plan_kernel(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first) {
+plan_kernel(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first, int *order) {
     __shared__ int part[32];
     __shared__ int base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -407,10 +412,20 @@ plan_kernel(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *
         __syncthreads();
     }
     if (tid == 0) first[N] = base;
+    if (!order) return;
+    __shared__ int lens[kOrdered];
+    static_assert(kOrdered == 1024, "a thread per segment");
+    const int total = min(base, bound), mine = tid < total ? table[tid].z : -1;
+    lens[tid] = mine;
+    __syncthreads();
+    int at = 0;
+    for (int s = 0; s < total; ++s) at += lens[s] > mine || (lens[s] == mine && s < tid);
+    if (tid < bound) order[tid < total ? at : tid] = tid;
 }
 
-cudaError_t launch_plan(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first, cudaStream_t stream) {
-    plan_kernel<<<1, 1024, 0, stream>>>(cu, N, seg_len, bound, table, first);
+cudaError_t launch_plan(const int32_t *cu, int N, int seg_len, int bound, int4 *table, int *first, int *order,
+                        cudaStream_t stream) {
+    plan_kernel<<<1, 1024, 0, stream>>>(cu, N, seg_len, bound, table, first, order);
     return cudaGetLastError();
 }
 cudaError_t launch_combine(float *seg_state, const float *seg_decay, const float *h0, float *hT, int N, int HV, int elems,
@@ -423,7 +438,7 @@ cudaError_t launch_combine(float *seg_state, const float *seg_decay, const float
 struct Cut {
     int seg_len, nseg;      // tokens per segment; segments per sequence (without cu_seqlens)
     int bound;              // segments at most, over all sequences
-    size_t table, first, decay, state, total;   // byte offsets in the workspace
+    size_t table, first, order, decay, state, total;   // byte offsets in the workspace
 };
 
 // warps per CTA of a head with `rows` rows per thread
@@ -457,6 +472,8 @@ static Cut cut_rows(const SsmArgs &a) {
     if (packed) off += up((size_t)bound * sizeof(int4));
     c.first = off;
     if (packed) off += up((size_t)(a.N + 1) * sizeof(int));
+    c.order = off;
+    if (packed && bound <= kOrdered) off += up((size_t)bound * sizeof(int));
     c.decay = off;
     c.state = off;
     if (packed || c.nseg > 1) {
@@ -488,8 +505,10 @@ static cudaError_t launch_rows_of(const SsmArgs &a, cudaStream_t stream) {
     if (packed) {
         p.map.table = reinterpret_cast<int4 *>(ws + cut.table);
         p.map.first = reinterpret_cast<int *>(ws + cut.first);
+        int *order = cut.bound <= kOrdered ? reinterpret_cast<int *>(ws + cut.order) : nullptr;
+        p.map.order = order;
         err = launch_plan(a.cu_seqlens, a.N, cut.seg_len, cut.bound, reinterpret_cast<int4 *>(ws + cut.table),
-                          reinterpret_cast<int *>(ws + cut.first), stream);
+                          reinterpret_cast<int *>(ws + cut.first), order, stream);
         if (err != cudaSuccess) return err;
     }
     const int warps = warps_of(DK, a.dv, ROWS);

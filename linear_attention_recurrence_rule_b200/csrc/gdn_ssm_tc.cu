@@ -306,7 +306,8 @@ states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cfg::O_BAR + 8 * SB_COUNT + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.HV / NH;
-    const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
+    int slot = blockIdx.x / tiles;
+    const int head = (blockIdx.x - slot * tiles) * NH;
     let_next_start();
     // (no wait gives up within the first second)
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
@@ -597,7 +598,8 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
     BlockTable *blocks = reinterpret_cast<BlockTable *>(sm + Cfg::O_BAR + 384);   // [NT][NH]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.HV / NH;
-    const int slot = blockIdx.x / tiles, head = (blockIdx.x - slot * tiles) * NH;
+    int slot = blockIdx.x / tiles;
+    const int head = (blockIdx.x - slot * tiles) * NH;
     if (blockIdx.x == 0 && threadIdx.x == 0 && !p.chained) *p.status = 0u;
     const Seg seg = find_seg(p.map, slot);
     if (!seg.ok || seg.len <= 0) return;
@@ -1092,7 +1094,7 @@ int heads_per_tile(const SsmArgs &a) { return a.dv == 64 && (a.HV / a.HK) % 2 ==
 struct TcCut {
     int seg_len, nseg;
     int64_t bound;
-    size_t table, first, decay, state, total;
+    size_t table, first, order, decay, state, total;
 };
 
 // Segment length in chunks: the fewest waves of CTAs over the SMs times the chunks of
@@ -1121,6 +1123,8 @@ TcCut cut_tc(const SsmArgs &a) {
     if (packed) off += up((size_t)c.bound * sizeof(int4));
     c.first = off;
     if (packed) off += up((size_t)(a.N + 1) * sizeof(int));
+    c.order = off;
+    if (packed && c.bound <= kOrdered) off += up((size_t)c.bound * sizeof(int));
     c.decay = off;
     off += up((size_t)c.bound * a.HV * sizeof(float));
     c.state = off;
@@ -1150,8 +1154,10 @@ cudaError_t launch_tiles(const SsmArgs &a, cudaStream_t stream) {
     if (packed) {
         p.map.table = reinterpret_cast<int4 *>(ws + cut.table);
         p.map.first = reinterpret_cast<int *>(ws + cut.first);
+        int *order = cut.bound <= kOrdered ? reinterpret_cast<int *>(ws + cut.order) : nullptr;
+        p.map.order = order;
         err = launch_plan(a.cu_seqlens, a.N, cut.seg_len, (int)cut.bound, reinterpret_cast<int4 *>(ws + cut.table),
-                          reinterpret_cast<int *>(ws + cut.first), stream);
+                          reinterpret_cast<int *>(ws + cut.first), order, stream);
         if (err != cudaSuccess) return err;
     }
     const uint64_t tokens = (uint64_t)(packed ? a.T : (int64_t)a.N * a.T);

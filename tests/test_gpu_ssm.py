@@ -158,6 +158,18 @@ def test_many_sequences(dtype, dk, dv):
     check_scan(y, hT, oracle(p, 1, 1, dk, dv, True), dtype, on_tensor_cores(dk, dv, dtype))
 
 
+@pytest.mark.parametrize("dtype,dk,dv", [(F32, 32, 32), (BF16, 128, 64)])
+def test_long_sequences_between_many_short_ones(dtype, dk, dv):
+    # nearly as many segments as are put in order: the long ones come last in the batch
+    gen = np.random.RandomState(1)
+    lengths = [int(v) for v in gen.randint(0, 3, 980)] + [700, 0, 1500, 129]
+    p = make_scan(lengths, 1, 2, dk, dv, dtype, seed=3)
+    if dk == 128:
+        p["h0"] = 0.1 * p["h0"]
+    y, hT = run(p, 1, 2, dk, dv, softplus=True)
+    check_scan(y, hT, oracle(p, 1, 2, dk, dv, True), dtype, on_tensor_cores(dk, dv, dtype))
+
+
 def test_without_final_state_and_optional_vectors():
     for dtype, dk, dv in ((F32, 64, 64), (BF16, 128, 128)):
         p = make_scan([700], 1, 2, dk, dv, dtype, seed=9, packed=False, h0=False)
