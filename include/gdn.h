@@ -547,9 +547,9 @@ GDN_API gdn_status gdn_chunk_prefill_layer(const void *q, const void *k, const v
  *
  * a[h] <= 0 and delta_t >= 0 are expected (decays in [0, 1]); nothing checks them,
  * and growing states may overflow (on the CUDA cores a state stands for up to 2^60 times
- * its size on the way: elements beyond 2^67 may).  Inputs have to be finite: a NaN or an infinity
- * in a token of a sequence may reach every output of its 128-token chunk and all
- * later ones (no other sequence, and nothing in rows behind the last sequence).
+ * its size on the way: elements beyond 2^67 may).  Inputs have to be finite: a NaN or
+ * an infinity in a token of a sequence may reach every output of its 128-token chunk and
+ * all later ones (no other sequence, and nothing in rows behind the last sequence).
  */
 #define GDN_SSM_SOFTPLUS 32u
 
