@@ -602,7 +602,13 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
     const int head = (blockIdx.x - slot * tiles) * NH;
     if (blockIdx.x == 0 && threadIdx.x == 0 && !p.chained) *p.status = 0u;
     const Seg seg = find_seg(p.map, slot);
-    if (!seg.ok || seg.len <= 0) return;
+    if (!seg.ok || seg.len <= 0) {
+        // The grid is done when its CTAs are, and what follows it in the stream then starts:
+        // where no segment has a token (a packed batch of empty sequences) these CTAs are all
+        // there are, and the kernels that still write hT and read the table have to be done too.
+        if (p.chained) wait_for_previous();
+        return;
+    }
     const int nch = (seg.len + L - 1) / L, last = nch - 1;
     const int tail = seg.len - last * L;      // tokens of the last chunk
     if (threadIdx.x == 0) {

@@ -146,6 +146,34 @@ def test_empty_calls():
     assert y.numel() == 0 and hT.shape == (0, 2, 64, 64)
 
 
+@pytest.mark.parametrize("dtype,dk,dv", [(F32, 32, 32), (F32, 128, 128), (BF16, 64, 64), (BF16, 128, 64),
+                                         (BF16, 128, 128)])
+@pytest.mark.parametrize("N", [1, 200, 1500])
+def test_batches_of_empty_sequences_with_rows_behind_them(dtype, dk, dv, N):
+    # no CTA of the scan has a token: what is launched behind the call must still find hT
+    # written and the workspace free (the next call rewrites both at once)
+    HK, HV, T, rounds = 1, 2, 300, 20
+    p = make_scan([0] * N, HK, HV, dk, dv, dtype, seed=N, pad=T)
+    p["row"].fill_(float("nan"))
+    g = to_cuda(p)
+    x, b, c = split_row(g["row"], HK, HV, dk, dv)
+    n = gdn.gdn_ssm_prefill_workspace_size(N, T, HK, HV, dk, dv, dtype, True)
+    ws = torch.zeros(max(n, 16), dtype=torch.uint8, device="cuda")
+    y = torch.full((1, T, HV, dv), 7.0, dtype=dtype, device="cuda")
+    h0 = [torch.randn(N, HV, dv, dk, device="cuda") for _ in range(rounds)]
+    hT = torch.zeros_like(h0[0])
+    copies = []
+    for h in h0:
+        gdn.gdn_ssm_prefill(x, b, c, g["dt"], g["a"], d=g["d"], dt_bias=g["dt_bias"], h0=h,
+                            cu_seqlens=g["cu_seqlens"], softplus=True, y=y, hT=hT, workspace=ws)
+        copies.append(hT.clone())
+    torch.cuda.synchronize()
+    assert bool((y == 7).all())
+    for h, got in zip(h0, copies):
+        assert torch.equal(h, got)
+    assert gdn.gdn_read_status(ws) == 0
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [(F32, 32, 32), (BF16, 128, 128)])
 def test_many_sequences(dtype, dk, dv):
     # more sequences than one block of the segment table takes at a time
