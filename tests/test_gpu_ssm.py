@@ -174,6 +174,30 @@ def test_batches_of_empty_sequences_with_rows_behind_them(dtype, dk, dv, N):
     assert gdn.gdn_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("dk,dv", [(32, 32), (128, 128)])
+@pytest.mark.parametrize("HV,T", [(8, 8192), (300, 1024)])
+def test_decays_near_one_do_not_drift(dk, dv, HV, T):
+    """Equal step sizes, so that every rounding of a decay points the same way, and no inputs:
+    the state is h0 times one decay.  Allowed, in units of 2^-24 relative: one for each tile of
+    16 tokens (the states' product), one for each of at most T / 128 segments (their chaining), 8
+    for the last tile's decay and the product of all tiles' against its exponential, and 10 |log
+    decay| (a product, four sums and an exponential behind each log, doubled for expm1f's slope).
+    One rounding of each token's decay would be up to T / 2."""
+    gen = torch.Generator().manual_seed(dk)
+    a = -torch.linspace(0.5, 1.5, HV) / T
+    h0 = 1 + torch.rand(1, HV, dv, dk, generator=gen)
+    x, k = torch.zeros(1, T, HV, dv), torch.zeros(1, T, 1, dk)
+    k[0, :, 0, 3] = 1.0
+    y, hT = gdn.gdn_ssm_prefill(x.cuda(), k.cuda(), k.cuda(), torch.ones(1, T, HV).cuda(), a.cuda(), h0=h0.cuda())
+    log = np.arange(1, T + 1)[:, None] * S.f64(a)
+    units = T / 16 + T / 128 + 8 + 10 * np.abs(log[-1])
+    ref = np.exp(log[-1])[None, :, None, None] * S.f64(h0)
+    within(hT, ref, U32 * units[:, None, None] * ref, "hT")
+    # the read-out multiplies once more, by the decays inside its tile
+    ref = np.exp(log)[None, :, :, None] * S.f64(h0)[:, None, :, :, 3]
+    within(y, ref, U32 * (units[:, None] + 8) * ref, "y")
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [(F32, 32, 32), (BF16, 128, 128)])
 def test_many_sequences(dtype, dk, dv):
     # more sequences than one block of the segment table takes at a time
