@@ -32,11 +32,12 @@
 // tensor memory columns), state (S -> bf16 operand, S times e^{G_L}), weight (w x, in
 // pieces of 32 tokens through a ring of 3) and output.  The mask takes e^{G_i-G_j} as the
 // decays behind j in its 32-token block times those from there to i, both <= 1: one
-// exponential per row and block (the diagonal blocks one per element where their decays
-// are too strong for a common reference).  All sums of log decays run over the tokens
-// between the two ends (block sums), none is a difference of running sums: a token that
-// forgets everything (a log decay of thousands) would leave such differences few digits
-// for the tokens behind it.
+// exponential per row and block.  On the diagonal a block whose log2 decays add up to no less
+// than -100 has a common reference, its start (an exponential of a running sum over another
+// one: off by up to 5e-5, beside the score's rounding to bf16 of 2^-8); stronger ones take one
+// exponential per element.  All other sums of log decays run over the tokens between the two
+// ends (block sums): a token that forgets everything (a log decay of thousands) would leave
+// differences of running sums few digits for the tokens behind it.
 //
 // y leaves through the x tile: the output warps put their rows over the x they have read
 // and TMA stores the tile (a part chunk is stored by the warps).  Their own stores, 32
@@ -213,9 +214,10 @@ struct HeadTab {
 // Step size and log2 decay of a token; no token: both 0.  A log2 decay below -150 is
 // taken as -150: every factor with that token in it is 0 in fp32 either way, and the
 // sums of the tokens around it keep their digits.
+__device__ __forceinline__ float log_decay(float delta, float ah) { return fmaxf(delta * ah, -150.f); }
 __device__ __forceinline__ void token_step(float dt, const HeadTab &t, bool in, bool soft, float &delta, float &g) {
     delta = in ? step_size(dt, t.bias, soft) : 0.f;
-    g = in ? fmaxf(delta * t.ah, -150.f) : 0.f;
+    g = in ? log_decay(delta, t.ah) : 0.f;
 }
 // Sums of g inside a 32-token block, a token per lane: `pre` up to and including the
 // token, `suf` behind it; returns the block's sum.  Sums over longer spans add whole
@@ -884,16 +886,22 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
                             }
                         }
                     } else {
-                        const float4 *pj = reinterpret_cast<const float4 *>(t->run + 32 * q);
+                        // the sums from j + 1 to i one after the other, from j = i down (a running
+                        // sum of thousands would leave their differences 12 bits)
                         const float4 *dj = reinterpret_cast<const float4 *>(t->diag + 32 * q);
+                        const float ah = __ldg(p.a + head + e) * kLog2e;
+                        float sum = 0.f;
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const float4 g4 = pj[u], d4 = dj[u];
-                            const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
+                        for (int u = 7; u >= 0; --u) {
+                            const float4 d4 = dj[u];
+                            const float ds[4] = {d4.x, d4.y, d4.z, d4.w};
                             float f[4];
 #pragma unroll
-                            for (int b = 0; b < 4; ++b)
-                                f[b] = 4 * u + b <= lane ? v[4 * u + b] * (ds[b] * ex2(pi - gs[b])) : 0.f;
+                            for (int b = 3; b >= 0; --b) {
+                                const bool in = 4 * u + b <= lane;
+                                f[b] = in ? v[4 * u + b] * (ds[b] * ex2(sum)) : 0.f;
+                                sum += in ? log_decay(ds[b], ah) : 0.f;
+                            }
                             out[2 * u] = pack_bf16x2(f[0], f[1]);
                             out[2 * u + 1] = pack_bf16x2(f[2], f[3]);
                         }

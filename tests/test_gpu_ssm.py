@@ -198,6 +198,32 @@ def test_decays_near_one_do_not_drift(dk, dv, HV, T):
     within(y, ref, U32 * (units[:, None] + 8) * ref, "y")
 
 
+@pytest.mark.parametrize("HV,dv", [(1, 128), (2, 64), (3, 64)])
+@pytest.mark.parametrize("resets", [0, 1, 12, 31])
+def test_each_score_is_rounded_once(HV, dv, resets):
+    """x is the identity and b = c a unit vector, so y[i, j] is the score of tokens i and j alone,
+    delta_j e^(decays behind j, up to i): exact but for its own rounding to bf16 (half a step of
+    the value's binade) and fp32 errors: 40 roundings of its log2 decay, 16 for the rest.  In
+    every 32 tokens the first `resets` of them forget everything, which must cost the scores of
+    the tokens behind them no digits (nothing but a factor with one of them in it is 0)."""
+    gen = torch.Generator().manual_seed(resets)
+    dt = 0.02 + 0.3 * torch.rand(1, dv, HV, generator=gen)
+    dt[:, torch.arange(dv) % 32 < resets] = 300.0
+    a = -(0.3 + torch.rand(HV, generator=gen))
+    x = torch.eye(dv).view(1, dv, 1, dv).expand(1, dv, HV, dv).to(BF16).contiguous()
+    k = torch.zeros(1, dv, 1, 128, dtype=BF16)
+    k[..., 5] = 1
+    y, _ = gdn.gdn_ssm_prefill(x.cuda(), k.cuda(), k.cuda(), dt.cuda(), a.cuda())
+    y, delta = S.f64(y)[0], S.f64(dt)[0]
+    run = np.cumsum(delta * S.f64(a), axis=0)
+    log = np.where(np.tri(dv, dtype=bool)[:, None], run[:, :, None] - run.T[None], -np.inf)     # [i, h, j]
+    ref = np.exp(log) * delta.T[None]
+    top = np.maximum(np.abs(y), ref)
+    half = 2.0 ** (np.floor(np.log2(np.maximum(top, 1e-37))) - 8)
+    units = 40 * np.abs(np.where(ref > 0, log, 0)) / np.log(2) + 16
+    within(torch.from_numpy(y), ref, half + U32 * units * ref + 1e-37, "scores")
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [(F32, 32, 32), (BF16, 128, 128)])
 def test_many_sequences(dtype, dk, dv):
     # more sequences than one block of the segment table takes at a time
