@@ -569,8 +569,8 @@ GDN_API gdn_status gdn_chunk_prefill_layer(const void *q, const void *k, const v
  * No output may overlap an input or another output (but hT may be h0).
  * workspace: device scratch of gdn_ssm_prefill_workspace_size(...) bytes (may be NULL
  * where that is 0), not to be shared by calls that may overlap; gdn_read_status as
- * after gdn_chunk_prefill (where the size is not 0).  It holds a state per segment: long
- * sequences are cut until the SMs are filled, packed ones at most into T / segment + N.
+ * after gdn_chunk_prefill (where the size is not 0).  It holds a state per sequence and for
+ * the segments that long sequences are cut into until the SMs are filled (at most 78 MB).
  * bf16 with dk = 128 and dv 64 or 128 runs on the tensor cores (y: a term is rounded to
  * bf16 once on the way, one from an earlier chunk of 128 tokens three times, by at most
  * 2^-8 of its size each; hT: fp32 accuracy),
@@ -585,7 +585,11 @@ GDN_API gdn_status gdn_ssm_prefill(const void *x, const void *b, const void *c, 
                                    float *hT, void *workspace, size_t workspace_bytes,
                                    gdn_stream_t stream);
 
-/* Bytes of device workspace gdn_ssm_prefill needs (0 also for sizes it would reject). */
+/*
+ * Bytes of device workspace for gdn_ssm_prefill (0 also for sizes it would reject).  Never
+ * less for more sequences or tokens: a workspace of this size also serves every call of at
+ * most N sequences and T tokens with the same heads, dims, dtype and form (varlen).
+ */
 GDN_API size_t gdn_ssm_prefill_workspace_size(int N, int64_t T, int HK, int HV, int dk, int dv,
                                               gdn_dtype dtype, int varlen);
 

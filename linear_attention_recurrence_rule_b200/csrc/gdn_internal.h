@@ -188,7 +188,8 @@ struct SsmStepArgs {
     void *workspace;
 };
 bool ssm_supported(int dk, int dv);
-size_t ssm_workspace_bytes(const SsmArgs &a);
+size_t ssm_workspace_bytes(const SsmArgs &a);   // never less than a call of fewer sequences or tokens needs
+bool ssm_uses_workspace(const SsmArgs &a);
 cudaError_t launch_ssm_prefill(const SsmArgs &a, cudaStream_t stream);
 size_t ssm_step_workspace_bytes(int N, int HK, int HV, int dk, int dv);
 cudaError_t launch_ssm_step(const SsmStepArgs &a, cudaStream_t stream);

@@ -85,7 +85,10 @@ gdn_status gdn_ssm_prefill(const void *x, const void *b, const void *c, const fl
     gdn::SsmArgs s{x, b, c, dt, a, d, dt_bias, h0, cu_seqlens, N, T, HK, HV, dk, dv, x_row, b_row, c_row,
                    dtype, (flags & GDN_SSM_SOFTPLUS) != 0, y, hT, workspace, workspace_bytes};
     const size_t need = gdn::ssm_workspace_bytes(s);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (need > 0 && (!workspace || workspace_bytes < need)) {
+        if (gdn::ssm_uses_workspace(s)) return GDN_ERR_WORKSPACE;
+        s.workspace = nullptr;   // room for smaller calls only; this one leaves no status either
+    }
     if (!aligned(workspace, 16)) return GDN_ERR_ALIGNMENT;
     const cudaError_t err = gdn::launch_ssm_prefill(s, reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

@@ -471,6 +471,7 @@ cudaError_t launch_combine(float *seg_state, const float *seg_decay, const float
 struct Cut {
     int seg_len, nseg;      // tokens per segment; segments per sequence (without cu_seqlens)
     int bound;              // segments at most, over all sequences
+    bool used;              // the call needs its workspace
     size_t table, first, order, decay, state, total;   // byte offsets in the workspace
 };
 
@@ -484,12 +485,14 @@ static int ctas_per_state(const SsmArgs &a) {
 
 // Segments are worth their first pass (half of the second's arithmetic) while the SMs have
 // fewer than about 4 CTAs of 4 warps each without them; below 128 tokens a segment's start
-// and end states weigh as much as its tokens.
+// and end states weigh as much as its tokens.  The workspace has room for what any call of as
+// many sequences and tokens may take: their segments come to 592 CTAs at most, or are one a
+// sequence.
 static Cut cut_rows(const SsmArgs &a) {
     Cut c{};
     const bool packed = a.cu_seqlens != nullptr;
     const int64_t longest = a.T > 0 ? a.T : 1;
-    const int64_t base = (int64_t)a.HV * ctas_per_state(a) * (packed ? 1 : a.N);
+    const int64_t head = (int64_t)a.HV * ctas_per_state(a), base = head * (packed ? 1 : a.N);
     int64_t nseg = base >= 592 ? 1 : 592 / base;
     int64_t len = (longest + nseg - 1) / nseg;
     len = (len + kTile - 1) / kTile * kTile;
@@ -497,24 +500,27 @@ static Cut cut_rows(const SsmArgs &a) {
     if (len > (1 << 30)) len = 1 << 30;
     c.seg_len = (int)len;
     c.nseg = (int)((longest + len - 1) / len);
-    const int64_t bound = packed ? a.T / len + a.N : (int64_t)a.N * c.nseg;
+    // (a sequence of l > 0 tokens has 1 + (l - 1) / seg_len segments)
+    const int64_t bound = packed ? (int64_t)a.N + c.nseg - 1 : (int64_t)a.N * c.nseg;
     c.bound = bound * a.HV * 4 > 0x7fffffff ? -1 : (int)bound;   // grid.x
+    c.used = packed || c.nseg > 1;
+    const int64_t parts = (longest + 127) / 128, most = 592 / head > 1 ? 592 / head : 1;
+    int64_t slots = packed ? a.N + min(most, parts) - 1 : max((int64_t)a.N, min(most, a.N * parts));
+    if (slots < bound) slots = bound;    // (more than 2^30 tokens in a sequence)
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     size_t off = 256;
     c.table = off;
-    if (packed) off += up((size_t)bound * sizeof(int4));
+    if (packed) off += up((size_t)slots * sizeof(int4));
     c.first = off;
     if (packed) off += up((size_t)(a.N + 1) * sizeof(int));
     c.order = off;
-    if (packed && bound <= kOrdered) off += up((size_t)bound * sizeof(int));
+    if (packed) off += up((size_t)min(slots, (int64_t)kOrdered) * sizeof(int));
     c.decay = off;
+    off += up((size_t)slots * a.HV * sizeof(float));
     c.state = off;
-    if (packed || c.nseg > 1) {
-        off += up((size_t)bound * a.HV * sizeof(float));
-        c.state = off;
-        off += (size_t)bound * a.HV * a.dv * a.dk * sizeof(float);
-    }
-    c.total = packed || c.nseg > 1 ? off : 0;
+    off += (size_t)slots * a.HV * a.dv * a.dk * sizeof(float);
+    // (one segment a sequence, in every smaller call too: nothing is kept between kernels)
+    c.total = packed || (most > 1 && parts > 1) ? off : 0;
     return c;
 }
 
@@ -528,10 +534,12 @@ static cudaError_t launch_rows_of(const SsmArgs &a, cudaStream_t stream) {
     RowParams p{a.x, a.b, a.c, a.dt, a.a, a.d, a.dt_bias, a.x_row, a.b_row, a.c_row, a.HK, a.HV, a.dv,
                 a.softplus, a.y, a.hT, a.h0, nullptr, nullptr, false,
                 SegMap{nullptr, nullptr, a.N, cut.nseg, a.T, cut.seg_len}};
-    if (cut.total) {
+    if (cut.total && ws) {
         // the status word of gdn_read_status: nothing waits on the device here
         err = cudaMemsetAsync(ws, 0, sizeof(unsigned int), stream);
         if (err != cudaSuccess) return err;
+    }
+    if (cut.used) {
         p.seg_decay = reinterpret_cast<float *>(ws + cut.decay);
         p.seg_state = reinterpret_cast<float *>(ws + cut.state);
     }
@@ -586,6 +594,7 @@ bool ssm_supported(int dk, int dv) {
 size_t ssm_workspace_bytes(const SsmArgs &a) {
     return ssm::tc_supported(a) ? ssm::tc_workspace_bytes(a) : ssm::cut_rows(a).total;
 }
+bool ssm_uses_workspace(const SsmArgs &a) { return ssm::tc_supported(a) || ssm::cut_rows(a).used; }
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, cudaStream_t stream) {
     using namespace ssm;

@@ -1112,15 +1112,22 @@ struct TcCut {
 };
 
 // Segment length in chunks: the fewest waves of CTAs over the SMs times the chunks of
-// a wave, a segment counting 2 chunks more for its start and end states.
+// a wave, a segment counting 2 chunks more for its start and end states.  That number of
+// segments goes up and down with T; the workspace has room for what any call of as many
+// sequences and tokens may take, so the cuts are held to kCutWaves waves of CTAs beyond one
+// segment a sequence.  (Of 4000 sizes up to 256K tokens 1.3% would take more to gain 2% of
+// the chunks; with half as many waves 7% would.  8 waves are 78 MB of states.)
+constexpr int kCutWaves = 8;
 TcCut cut_tc(const SsmArgs &a) {
     TcCut c{};
     const bool packed = a.cu_seqlens != nullptr;
     const int64_t chunks = (a.T + L - 1) / L > 0 ? (a.T + L - 1) / L : 1, seqs = packed ? 1 : a.N;
     const int64_t tiles = a.HV / heads_per_tile(a), sms = sm_count();
+    const int64_t more = kCutWaves * sms / tiles;     // segments beyond one a sequence
     int64_t best = 0, best_cost = 0;
     for (int64_t n = 1; n <= 64 && n <= chunks; ++n) {
         const int64_t len = (chunks + n - 1) / n, segs = (chunks + len - 1) / len;
+        if ((segs - 1) * seqs > more) continue;
         const int64_t waves = (segs * seqs * tiles + sms - 1) / sms;
         const int64_t cost = waves * (len + 2);
         if (best == 0 || cost < best_cost) {
@@ -1130,19 +1137,21 @@ TcCut cut_tc(const SsmArgs &a) {
     }
     c.seg_len = (int)(best * L);
     c.nseg = (int)((chunks + best - 1) / best);
-    c.bound = packed ? a.T / c.seg_len + a.N : (int64_t)a.N * c.nseg;
+    // (a sequence of l > 0 tokens has 1 + (l - 1) / seg_len segments)
+    c.bound = packed ? a.N + c.nseg - 1 : (int64_t)a.N * c.nseg;
+    const int64_t slots = a.N + min(more, (chunks - 1) * seqs);
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     size_t off = 256;
     c.table = off;
-    if (packed) off += up((size_t)c.bound * sizeof(int4));
+    if (packed) off += up((size_t)slots * sizeof(int4));
     c.first = off;
     if (packed) off += up((size_t)(a.N + 1) * sizeof(int));
     c.order = off;
-    if (packed && c.bound <= kOrdered) off += up((size_t)c.bound * sizeof(int));
+    if (packed) off += up((size_t)min(slots, (int64_t)kOrdered) * sizeof(int));
     c.decay = off;
-    off += up((size_t)c.bound * a.HV * sizeof(float));
+    off += up((size_t)slots * a.HV * sizeof(float));
     c.state = off;
-    off += (size_t)c.bound * a.HV * a.dv * DK * sizeof(float);
+    off += (size_t)slots * a.HV * a.dv * DK * sizeof(float);
     c.total = off;
     return c;
 }

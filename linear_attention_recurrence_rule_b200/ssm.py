@@ -93,7 +93,7 @@ def _raw_stream(dev):
 
 
 def gdn_ssm_prefill_workspace_size(N, T, HK, HV, dk, dv, dtype, varlen) -> int:
-    """Bytes of workspace ``gdn_ssm_prefill`` needs (0: none)."""
+    """Bytes of workspace for ``gdn_ssm_prefill`` with at most N sequences and T tokens (0: none)."""
     code = dtype if isinstance(dtype, int) else _code(torch.empty(0, dtype=dtype), "dtype")
     return int(load_library().gdn_ssm_prefill_workspace_size(
         int(N), int(T), int(HK), int(HV), int(dk), int(dv), code, int(bool(varlen))))

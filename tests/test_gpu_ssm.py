@@ -272,6 +272,25 @@ def test_results_repeat_bit_for_bit_and_streams():
         assert torch.equal(y, y2) and torch.equal(hT, h2)
 
 
+@pytest.mark.parametrize("dtype,dk,dv,HK,HV", [(BF16, 128, 128, 1, 4), (BF16, 128, 64, 4, 16), (BF16, 64, 64, 1, 2),
+                                               (F32, 128, 128, 1, 4), (F32, 32, 32, 1, 300)])
+def test_one_workspace_for_calls_of_many_sizes(dtype, dk, dv, HK, HV):
+    # sized for the largest: 5 sequences of 1200 tokens; smaller calls are cut otherwise, some finer
+    for packed in (False, True):
+        n = gdn.gdn_ssm_prefill_workspace_size(5, 6000 if packed else 1200, HK, HV, dk, dv, dtype, packed)
+        ws = torch.full((max(n, 16) + 64,), 255, dtype=torch.uint8, device="cuda")
+        behind = ws[max(n, 16):].clone()
+        for lengths in ([1200] * 5, [1152], [1037] * 2, [640] * 3, [130], [1], [384] * 5):
+            if packed and len(lengths) == 5:
+                lengths = [v + w for v, w in zip(lengths, (0, -5, 0, 5, 0))]
+            p = make_scan(lengths, HK, HV, dk, dv, dtype, seed=sum(lengths), packed=packed, step_mean=-4.0)
+            y, hT = run(p, HK, HV, dk, dv, softplus=True)
+            y2, h2 = run(p, HK, HV, dk, dv, softplus=True, workspace=ws[:n] if n else None)
+            assert torch.equal(y, y2) and torch.equal(hT, h2), lengths
+            assert not n or gdn.gdn_read_status(ws) == 0
+        assert torch.equal(ws[max(n, 16):], behind)
+
+
 def test_two_captured_graphs_with_their_own_workspaces():
     HK, HV, dk, dv = 1, 2, 128, 128
     n = gdn.gdn_ssm_prefill_workspace_size(2, 900, HK, HV, dk, dv, BF16, False)

@@ -67,6 +67,24 @@ def test_workspace_size_of_rejected_sizes(lib):
     assert f(0, 64, 1, 2, 128, 128, gdn.GDN_BF16, 1) == 0
 
 
+@pytest.mark.parametrize("dtype,dk,dv", [(gdn.GDN_BF16, 128, 128), (gdn.GDN_BF16, 128, 64), (gdn.GDN_BF16, 64, 64),
+                                         (gdn.GDN_F32, 32, 32), (gdn.GDN_F32, 128, 128)])
+@pytest.mark.parametrize("varlen", [0, 1])
+def test_workspace_of_a_larger_call_serves_smaller_ones(lib, dtype, dk, dv, varlen):
+    # the number of segments goes up and down with the sizes; the workspace must not
+    size = lib.gdn_ssm_prefill_workspace_size
+    for HK, HV in ((1, 1), (1, 3), (8, 32), (16, 32), (1, 24), (4, 128), (1, 300)):
+        for N in (1, 2, 7, 8, 64):
+            sizes = [size(N, T, HK, HV, dk, dv, dtype, varlen)
+                     for T in [*range(1, 3000, 31), *range(3000, 70000, 997), 1 << 20, 1 << 24]]
+            assert sizes == sorted(sizes), (HK, HV, N)
+        for T in (1, 129, 1152, 4096, 10368, 16384, 65536):
+            sizes = [size(N, T, HK, HV, dk, dv, dtype, varlen) for N in [*range(1, 130), 1000, 1023, 1024, 1025, 1100, 5000]]
+            assert sizes == sorted(sizes), (HK, HV, T)
+    # and no call is given less than its own segments need: a state each, one a sequence at least
+    assert size(7, 100, 1, 3, dk, dv, dtype, 1) >= 7 * 3 * dk * dv * 4
+
+
 def step(lib, **kw):
     a = dict(xbc=P(0x1000), dt=P(0x2000), a=P(0x3000), d=None, bias=None, w=P(0x4000), cb=None, cs=P(0x5000),
              co=P(0x5000), W=4, state=P(0x6000), out=P(0x6000), N=2, HK=1, HV=2, dk=128, dv=64, row=0, flags=0,
