@@ -604,7 +604,8 @@ GDN_API size_t gdn_ssm_prefill_workspace_size(int N, int64_t T, int HK, int HV, 
  *   dt [N][HV] fp32; a, d, dt_bias as above; state, state_out [N][HV][dv][dk] fp32
  *   (the same buffer: in place; otherwise they must not overlap); y [N][HV][dv] dtype
  * y must not overlap anything else.  flags: GDN_SSM_SOFTPLUS, GDN_CONV_SILU.
- * Supported: dk in {32, 64, 128}, 1 <= dv <= 256, widths as gdn_short_conv, N <= 262140.  Alignment: states and
+ * Supported: dk in {32, 64, 128}, 1 <= dv <= 256, widths as gdn_short_conv, N <= 262140,
+ * rows of at most 2^31 - 256 channels.  Alignment: states and
  * workspace 16 bytes, the rest their element's size.  workspace: device scratch of
  * gdn_ssm_step_workspace_size(...) bytes (the convolved row in fp32), not to be shared
  * by calls that may overlap.  Two launches, the second one dependent on the first.

@@ -28,8 +28,9 @@ gdn_status check_ssm_sizes(int N, int64_t T, int HK, int HV, int dk, int dv, gdn
 gdn_status check_step_sizes(int N, int HK, int HV, int dk, int dv) {
     if (N < 0 || HK <= 0 || HV <= 0 || dk <= 0 || dv <= 0 || HV % HK) return GDN_ERR_INVALID_ARG;
     if (!gdn::decode_supported(dk, dv)) return GDN_ERR_UNSUPPORTED;
-    // the row in 32 bits; sequences in groups of four over grid.y
-    if ((int64_t)N * HV > kGrid || (int64_t)HV * dv + 2 * (int64_t)HK * dk > kGrid || N > 4 * 65535)
+    // the row, rounded up to a block of 256 channels, in 32 bits; sequences in groups of four
+    // over grid.y
+    if ((int64_t)N * HV > kGrid || (int64_t)HV * dv + 2 * (int64_t)HK * dk > kGrid - 255 || N > 4 * 65535)
         return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }

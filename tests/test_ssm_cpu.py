@@ -119,6 +119,15 @@ def test_step_refusals(lib):
     assert lib.gdn_ssm_step_workspace_size(2, 3, 2, 128, 64) == 0
 
 
+def test_step_refuses_rows_past_32_bits(lib):
+    # a row is rounded up to blocks of 256 channels in 32 bits
+    rows = dict(N=1, HK=1, dk=32, dv=1)
+    assert step(lib, HV=(1 << 31) - 256 - 64, ws=None, **rows) == WORKSPACE
+    assert step(lib, HV=(1 << 31) - 255 - 64, **rows) == UNSUPPORTED
+    assert step(lib, HV=(1 << 31) - 1 - 64, **rows) == UNSUPPORTED
+    assert lib.gdn_ssm_step_workspace_size(1, 1, (1 << 31) - 1 - 64, 32, 1) == 0
+
+
 def gated(lib, **kw):
     a = dict(o=P(0x1000), z=P(0x2000), w=P(0x3000), rows=4, G=2, D=64, o_row=0, z_row=0, wg=1, eps=1e-6, flags=0,
              dtype=gdn.GDN_BF16, y=P(0x4000))
