@@ -572,7 +572,7 @@ GDN_API gdn_status gdn_chunk_prefill_layer(const void *q, const void *k, const v
  * after gdn_chunk_prefill (where the size is not 0).  It holds a state per sequence and for
  * the segments that long sequences are cut into until the SMs are filled (at most 78 MB).
  * bf16 with dk = 128 and dv 64 or 128 runs on the tensor cores (y: a term is rounded to
- * bf16 once on the way, one from an earlier chunk of 128 tokens three times, by at most
+ * bf16 once on the way, one from an earlier chunk of 128 tokens twice, by at most
  * 2^-8 of its size each; hT: fp32 accuracy),
  * everything else on the CUDA cores in fp32.  Up to five launches on `stream`.
  * N == 0: GDN_OK, nothing launched.  T == 0: hT gets h0 (or zero).

@@ -19,9 +19,13 @@
 //  * combine_kernel (gdn_ssm_rows.cu): chains the segments in place; hT.
 //  * scan_kernel, one CTA per (segment, value tile), chunk by chunk: C B^T, the masked
 //    and decayed P, C S^T, P X and the next state, all on tcgen05 with the state in
-//    tensor memory.  Its state only feeds the bf16 y: w_j, w_j x_j, S and P are rounded
-//    to bf16, so a term of y inside its chunk is rounded once on the way and one from
-//    before it three times (w_j in bf16 makes the weighting one packed multiply).
+//    tensor memory.  Its state only feeds the bf16 y: P, w_j x_j and the S that is read out are
+//    rounded to bf16, as the operands of its products, so a term of y inside its chunk is
+//    rounded once on the way and one from before it twice.  y of the measured cases is off
+//    by 1.83e-3 to 1.91e-3 in norm where the output's own rounding is 1.66e-3; the rest is
+//    nearly all P's, a second product with P's remainder would take a quarter of the tensor
+//    cores' time more and tensor memory that pairs of heads do not have.  (w_j in bf16 too, one
+//    packed multiply for four instructions, was 1% faster, for a third rounding.)
 //
 // A value tile is 128 columns where it can be: one head of 128, or two heads of 64 of
 // one group, which share C B^T and the loads of b and c; else one head of 64.
@@ -202,9 +206,10 @@ __device__ __forceinline__ float2 subp(float2 a, float2 b) {
     memcpy(&d, &ud, 8);
     return d;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, __nv_bfloat162 w) {
-    const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), w);
-    return *reinterpret_cast<const uint32_t *>(&p);
+// w x of a bf16 pair, rounded once
+__device__ __forceinline__ uint32_t weighted(uint32_t x, float w) {
+    const float2 f = mulp(unpack2(x), make_float2(w, w));
+    return pack_bf16x2(f.x, f.y);
 }
 
 // One head's decay and step bias, a * log2 e and dt_bias.
@@ -985,9 +990,9 @@ scan_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CU
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint4 u = lds128(src + v * 16384 + half * 2048);
-                        const __nv_bfloat162 w = __float2bfloat162_rn(tab[16 * half] * behind);
-                        sts128(dst + v * 4096 + half * 2048, mul_bf16x2(u.x, w), mul_bf16x2(u.y, w), mul_bf16x2(u.z, w),
-                               mul_bf16x2(u.w, w));
+                        const float w = tab[16 * half] * behind;
+                        sts128(dst + v * 4096 + half * 2048, weighted(u.x, w), weighted(u.y, w), weighted(u.z, w),
+                               weighted(u.w, w));
                     }
                 }
                 fence_proxy_async_smem();

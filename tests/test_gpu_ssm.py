@@ -224,6 +224,37 @@ def test_each_score_is_rounded_once(HV, dv, resets):
     within(torch.from_numpy(y), ref, half + U32 * units * ref + 1e-37, "scores")
 
 
+@pytest.mark.parametrize("HV,dv", [(148, 128), (296, 64), (147, 64)])
+def test_each_carried_value_is_rounded_once(HV, dv):
+    """One token's value in every column and b = c a unit vector: behind the first chunk of 128
+    tokens y[i, j] is the value of token j alone, weighted to the chunk's end (rounded to bf16:
+    half a step of its binade), decayed on, and rounded for the output.  fp32 on the way: 40
+    roundings of the log2 decay, 24 for the rest.  (Heads enough that no sequence is cut.)"""
+    gen = torch.Generator().manual_seed(HV)
+    T, L = 200, 128
+    dt = 0.01 + 0.1 * torch.rand(1, T, HV, generator=gen)
+    a = -(0.2 + 0.8 * torch.rand(HV, generator=gen))
+    value = (1 + torch.rand(HV, dv, generator=gen)).to(BF16)
+    x = torch.zeros(1, T, HV, dv, dtype=BF16)
+    j = torch.arange(dv)
+    x[0, j, :, j] = value.t()
+    k = torch.zeros(1, T, 1, 128, dtype=BF16)
+    k[..., 9] = 1
+    y, _ = gdn.gdn_ssm_prefill(x.cuda(), k.cuda(), k.cuda(), dt.cuda(), a.cuda())
+    y, delta = S.f64(y)[0, L:], S.f64(dt)[0]
+    run = np.cumsum(delta * S.f64(a), axis=0)                                       # [t, h]
+    end = run[L - 1]
+    weighted = delta[:dv].T * np.exp(end[:, None] - run[:dv].T) * S.f64(value)       # [h, j]
+    on = np.exp(run[L:] - end)[:, :, None]
+    ref = on * weighted
+
+    def half(v):
+        return 2.0 ** (np.floor(np.log2(v)) - 8)
+    log = np.abs(run[L:, :, None] - run[:dv].T) / np.log(2)
+    allow = half(np.maximum(np.abs(y), ref)) + on * half(weighted) + U32 * (40 * log + 24) * ref
+    within(torch.from_numpy(y), ref, allow, "carried")
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [(F32, 32, 32), (BF16, 128, 128)])
 def test_many_sequences(dtype, dk, dv):
     # more sequences than one block of the segment table takes at a time
