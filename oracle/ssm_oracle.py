@@ -71,6 +71,47 @@ def scan(x, b, c, dt, a, d=None, dt_bias=None, h0=None, cu_seqlens=None, soft=Fa
     return y, hT, y_abs, y_units, h_units
 
 
+def chunk_terms(x, b, c, dt, a, dt_bias=None, h0=None, cu_seqlens=None, soft=False, chunk=128):
+    """How y comes about when a sequence is run in chunks: per output sum |terms| of its own
+    chunk, sum |terms| from before it, and the sum of the squares of what an evaluation with
+    rounded scores, weighted values and states rounds -- each score times its value, each
+    weighted value's and each state element's part of the output."""
+    x, b, c, dt, a = f64(x), f64(b), f64(c), f64(dt), f64(a)
+    B, T, HV, dv = x.shape
+    HK, dk = b.shape[2:]
+    delta = dt + (0 if dt_bias is None else f64(dt_bias))
+    delta = softplus(delta) if soft else delta
+    if cu_seqlens is None:
+        spans = [(n, n, 0, T) for n in range(B)]
+    else:
+        cu = [int(v) for v in cu_seqlens]
+        spans = [(n, 0, cu[n], cu[n + 1]) for n in range(len(cu) - 1)]
+    near, far, squares = np.zeros(x.shape), np.zeros(x.shape), np.zeros(x.shape)
+    for n, row, t0, t1 in spans:
+        for h in range(HV):
+            g = h // (HV // HK)
+            S = np.zeros((dv, dk)) if h0 is None else f64(h0)[n, h].copy()
+            A, V = np.abs(S), np.zeros((dv, dk, dk))     # sum |terms|; sum of w^2 x^2 b b^T
+            for s in range(t0, t1, chunk):
+                at = slice(s, min(s + chunk, t1))
+                X, Bm, Cm, dl = x[row, at, h], b[row, at, g], c[row, at, g], delta[row, at, h]
+                run = np.cumsum(dl * a[h])
+                low = np.tri(len(run), dtype=bool)
+                score = np.exp(np.where(low, run[:, None] - run[None], -np.inf)) * dl * (Cm @ Bm.T)
+                into = np.exp(run)[:, None]
+                terms = np.exp(np.where(low, run[:, None] - run[None], -np.inf)) * dl * (np.abs(Cm) @ np.abs(Bm).T)
+                near[row, at, h] = terms @ np.abs(X)
+                far[row, at, h] = into * (np.abs(Cm) @ A.T)
+                squares[row, at, h] = (score ** 2) @ (X ** 2) + into ** 2 * (
+                    (Cm ** 2) @ (S ** 2).T + np.einsum("tk,vkl,tl->tv", Cm, V, Cm, optimize=True))
+                w = dl * np.exp(run[-1] - run)
+                keep = np.exp(run[-1])
+                S = keep * S + (w[:, None] * X).T @ Bm
+                A = keep * A + (w[:, None] * np.abs(X)).T @ np.abs(Bm)
+                V = keep ** 2 * V + np.einsum("tv,tk,tl->vkl", (w[:, None] * X) ** 2, Bm, Bm, optimize=True)
+    return near, far, squares
+
+
 def conv_token(row, weight, bias, state, silu):
     """One token of the short convolution: row [N,C], state [N,W-1,C] -> out, new state."""
     row, weight, state = f64(row), f64(weight), f64(state)

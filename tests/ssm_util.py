@@ -61,3 +61,40 @@ def check_scan(y, hT, ref, dtype, tensor_cores, what=""):
     within(y, r_y, allow + 1e-37, what + "y")
     if hT is not None:
         within(hT, r_h, 2 * U32 * h_units + 1e-37, what + "hT")
+
+
+def term_bounds(p, HK, HV, dk, dv, rate=1.0):
+    """Exact y and hT, the bound of each y and of each norm of y over a sequence and head.
+
+    A term of y inside its chunk of 128 tokens is rounded to bf16 once, one from before it twice
+    (its weighted value, the state), d x not at all; fp32 roundings as the oracle counts them,
+    doubled.  In norm a rounding of a value m 2^e, 1 <= m < 2, is uniform within 2^(e-8): its mean
+    square is at most (2^-8)^2 / 3 of the value's square, and the roundings are independent."""
+    x, b, c = split_row(p["row"], HK, HV, dk, dv)
+    y, h, _, y_units, h_units = S.scan(x, b, c, p["dt"], rate * S.f64(p["a"]), p["d"], p["dt_bias"], p["h0"],
+                                       p["cu_seqlens"], True)
+    near, far, squares = S.chunk_terms(x, b, c, p["dt"], rate * S.f64(p["a"]), p["dt_bias"], p["h0"], p["cu_seqlens"], True)
+    u = U[torch.bfloat16]
+    allow = u * np.abs(y) + 2 * U32 * (1 + u) * y_units + u * near + 2 * u * (1 + u) * far
+    norm = u / np.sqrt(3) * np.sqrt(y * y + squares) + 2 * U32 * y_units
+    return y, h, allow, norm, h_units
+
+
+def sequences(p):
+    if p["cu_seqlens"] is None:
+        B, T = p["dt"].shape[:2]
+        return [(n, slice(0, T)) for n in range(B)]
+    cu = [int(v) for v in p["cu_seqlens"]]
+    return [(0, slice(s, e)) for s, e in zip(cu, cu[1:]) if e > s]
+
+
+def in_norm(out, y, norm, where, least=2000):
+    """Whether every (sequence, head) of at least `least` outputs is within its norm's bound."""
+    err = S.f64(out) - y
+    ok = True
+    for n, t in where:
+        for h in range(y.shape[2]):
+            e, lim = err[n, t, h], norm[n, t, h]
+            if e.size >= least:
+                ok = ok and np.linalg.norm(e) <= np.linalg.norm(lim)
+    return ok

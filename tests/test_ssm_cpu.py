@@ -8,6 +8,7 @@ import torch
 
 from linear_attention_recurrence_rule_b200 import _build, gdn, ssm
 from oracle import ssm_oracle as S
+from ssm_util import in_norm, make_scan, sequences, split_row, term_bounds
 
 OK, INVALID, UNSUPPORTED, ALIGNMENT, WORKSPACE = (gdn.GDN_OK, gdn.GDN_ERR_INVALID_ARG, gdn.GDN_ERR_UNSUPPORTED,
                                                   gdn.GDN_ERR_ALIGNMENT, gdn.GDN_ERR_WORKSPACE)
@@ -252,6 +253,44 @@ def test_oracle_error_units_cover_fp32():
         worst = max(worst, err.max())
     assert worst <= 1 and worst > 1e-3
     assert (np.abs(s - h[0]) <= hu[0] * 2.0 ** -24).all()
+
+
+def test_oracle_chunk_terms():
+    # the two sums are the scan's sum of |terms| (without d x), whatever the chunk
+    p = make_scan([1, 70, 0, 45], 2, 4, 8, 6, torch.float32, seed=3)
+    parts = split_row(p["row"], 2, 4, 8, 6)
+    y, _, total, _, _ = S.scan(*parts, p["dt"], p["a"], None, p["dt_bias"], p["h0"], p["cu_seqlens"], True)
+    for chunk in (1, 32, 128):
+        near, far, squares = S.chunk_terms(*parts, p["dt"], p["a"], p["dt_bias"], p["h0"], p["cu_seqlens"], True, chunk)
+        assert np.allclose(near + far, total)
+        assert (squares <= 2 * (near ** 2 + far ** 2) * (1 + 1e-9)).all()
+    # roundings drawn at random leave errors of that mean square
+    rs, T, dv, dk = np.random.RandomState(0), 8, 4, 3
+    x, b, c, dt = rs.randn(1, T, 1, dv), rs.randn(1, T, 1, dk), rs.randn(1, T, 1, dk), rs.rand(1, T, 1)
+    a, h0 = np.array([-0.3]), rs.randn(1, 1, dv, dk)
+    exact = S.scan(x, b, c, dt, a, None, None, h0)[0][0, :, 0]
+    *_, squares = S.chunk_terms(x, b, c, dt, a, None, h0, chunk=4)
+    total, draws = np.zeros((T, dv)), 4000
+    eps = lambda *s: 1 + 1e-6 * rs.randn(draws, *s)   # noqa: E731
+    St, out = np.broadcast_to(h0[0, 0], (draws, dv, dk)), []
+    for s in (0, 4):
+        X, Bm, Cm, dl = x[0, s:s + 4, 0], b[0, s:s + 4, 0], c[0, s:s + 4, 0], dt[0, s:s + 4, 0]
+        g = np.cumsum(dl) * a[0]
+        P = np.tril(np.exp(g[:, None] - g[None]) * dl * (Cm @ Bm.T)) * eps(4, 4)
+        out.append(P @ X + np.exp(g)[:, None] * np.einsum("tk,nvk->ntv", Cm, St * eps(dv, dk)))
+        wx = (dl * np.exp(g[-1] - g))[:, None] * X * eps(4, dv)
+        St = np.exp(g[-1]) * St + np.einsum("ntv,tk->nvk", wx, Bm)
+    seen = ((np.concatenate(out, 1) - exact) ** 2).mean(0) / 1e-12
+    assert np.allclose(seen, squares[0, :, 0], rtol=0.15)     # 4000 draws: 2.2% standard error
+
+
+def test_bound_in_norm_is_not_idle():
+    # an exact result, rounded, is inside it; one with decay rates off by 2% is not
+    p = make_scan([1411], 1, 2, 128, 64, torch.bfloat16, seed=1, packed=False, step_mean=-4.0)
+    ref, _, _, norm, _ = term_bounds(p, 1, 2, 128, 64)
+    off, *_ = term_bounds(p, 1, 2, 128, 64, rate=1.02)
+    assert in_norm(torch.from_numpy(ref).to(torch.bfloat16), ref, norm, sequences(p))
+    assert not in_norm(torch.from_numpy(off).to(torch.bfloat16), ref, norm, sequences(p))
 
 
 def test_oracle_norms():
