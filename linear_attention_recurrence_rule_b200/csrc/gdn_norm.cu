@@ -10,7 +10,12 @@
 // (16-byte vectors) belongs to 8, 16 or 32 lanes of a warp where it fits in their
 // registers -- sums by shuffles, several rows per warp -- and to a whole block
 // otherwise.  Rows that are not made of aligned 16-byte vectors (odd D, odd strides)
-// take a kernel that reads element by element, three times at most.
+// take a kernel that reads element by element, three times at most, and so do rows of more
+// than 4096 vectors (64 KB).  Alone and with a cold L2, of the measured copy rate: gated norm
+// bf16 16384 x 2048 65%, 16384 x 2049 26%, 4096 groups of 32 x 100 6% (a block for each group
+// of 100); residual norm with an fp32 residual, 16384 x 2048 94%, 16384 x 2049 66%, 2048 x
+// 16384 62% (1024 threads leave 64 registers each, and the row's two fp32 copies spill), 512 x
+// 65536 24%.
 #include <type_traits>
 
 #include "gdn_common.cuh"

@@ -49,15 +49,16 @@
 // lower the clock).
 //
 // What bounds it (64K tokens, 32 heads of 128, 16 groups: 1.62 GB, 247 us at the measured
-// copy rate; 670 us in a long run, under the 1000 W cap, 570 to 620 us in a short one):
-// scan_kernel 358 us, states_kernel 203 us, combine_kernel 21 us.  scan_kernel takes about
-// 5000 cycles per 128 tokens, and no one pipe fills them: the tensor cores read 224 KB of
-// shared memory (1792 cycles at 128 bytes a cycle) and the schedulers issue 2400
-// instructions each; taking any one role's shared memory accesses out changed the time by
-// 5% at most, 13% fewer instructions by 0.5%.  What is left is the chain of one chunk:
-// C S^T, the load of c into its one tile, C B^T, the mask, P X, the read-out, and beside it
-// the state's way through the state warps and back.  A second c tile would shorten it; the
-// tiles of b, c, x and P fill the 227 KB.  Measured and not kept: eight weight warps (640 ->
+// copy rate; 660 to 680 us in a long run, under the 1000 W cap): scan_kernel 369 us,
+// states_kernel 203 us, combine_kernel 20 us, each alone.  scan_kernel takes about 5000 cycles
+// per 128 tokens, and no one pipe fills them: the tensor cores read 224 KB of shared memory
+// (1792 cycles at 128 bytes a cycle) and the schedulers issue 2400 instructions each (0.33 a
+// cycle); taking any one role's shared memory accesses out changed the time by 5% at most, 13%
+// fewer instructions by 0.5%.  What is left is the chain of one chunk: C S^T, the load of c
+// into its one tile, C B^T, the mask, P X, the read-out, and beside it the state's way through
+// the state warps and back.  Its order is a choice: C S^T waits for the read-out of the chunk
+// before because y has two accumulators and tensor memory no second pair, and the tiles of b,
+// c, x and P fill the 227 KB.  Measured and not kept: eight weight warps (640 ->
 // 665 us), eight output or state warps (683 -> 700 us), a skip term from L2 instead of the
 // shared x tile (740 -> 790 us), C S^T issued at whichever is ready first (565 -> 585 us),
 // roles unrolled in full (they miss the instruction cache: 740 us against 410 us rolled),
@@ -245,12 +246,12 @@ __device__ __forceinline__ float block_sums(float g, int lane, float &pre, float
 // S[value][key] += (w x)^T b over the tokens of the segment.  The workers take x^T out of
 // shared memory with transposing matrix loads, weight it and put it into tensor memory as
 // three bf16 terms (the A operand, lanes = value columns): the products then read only b
-// from shared memory, whose bandwidth is what bounds this kernel (with the terms in
-// shared memory it moved 384 KB per 128 tokens of a 128-wide tile instead of 192 KB, and
-// took 280 us instead of 214 us for 64K tokens of 32 heads of 128).  Its 24 products a
-// chunk take 1540 cycles, the workers' chain of a piece (load, split, store, signal) about
-// as long again.  The first terms and
-// the two small ones have an accumulator each, so that the small ones are not rounded
+// from shared memory (with the terms in shared memory it moved 384 KB per 128 tokens of a
+// 128-wide tile instead of 192 KB, and took 280 us instead of 214 us for 64K tokens of 32
+// heads of 128; 203 us now, its loads and stores there at 23% of their rate).  What bounds it:
+// its 24 products a chunk take 1540 cycles, the workers' chain of a piece (load, split, store,
+// signal) about as long again, and the two overlap in part; 0.47 of the issue slots are used.
+// The first terms and the two small ones have an accumulator each, so that the small ones are not rounded
 // away against the large sum, and every kFlush chunks both are added to sums in the
 // workers' registers: the tensor cores truncate, and over the 456 additions of a 7K-token
 // segment the sums fell short by 2.2e-6; over 64 by 3e-7.
