@@ -22,16 +22,18 @@
 // once at its end.  Nothing overflows within 2^60, and a sum keeps its relative accuracy
 // whatever it is divided by.  Stronger tiles take the plain form.
 //
-// In a tile whose log decays add up to less than 1/4 the Gammas are exponentials of the sums,
-// one rounding a tile and not one a token: a product of 1000 decays near 1, each rounded by
-// up to 2^-25, is off by up to 3e-5, all in one direction where the step sizes repeat.  What a
-// tile's decay was rounded by goes into the next tile's log, so the product of all of them
-// stays within two roundings of the exact one (8192 equal tokens, log decays of 0.5 to 1.5 in
-// all: states off by 4.3e-4 at worst, now 3.3e-6, their own roundings).  Stronger tiles
-// multiply their tokens' decays, whose errors the tokens next to each other share (a sum of 40
-// has few digits left for the differences); their states do not live to gather many roundings.
-// y of 2048 tokens with 32 heads of 128 (relative norm): 1.6e-7 to 9.1e-7, now 1.3e-7 to
-// 1.4e-7, for 236 -> 241 us.
+// As far into a tile as the log decays add up to less than 1/4, Gamma is the exponential of
+// the sum, one rounding a tile and not one a token: a product of 1000 decays near 1, each
+// rounded by up to 2^-25, is off by up to 3e-5, all in one direction where the step sizes
+// repeat.  What a tile's decay was rounded by goes into the next tile's log, so the product of
+// all of them stays within two roundings of the exact one (8192 equal tokens, log decays of 0.5
+// to 1.5 in all: states off by 4.3e-4 at worst, now 3.2e-6, their own roundings).  Farther on
+// Gamma is the product of the tokens' decays, whose errors neighbours share (a sum of 40 has few
+// digits left for the differences); such states do not live to gather many roundings.  y of 2048
+// tokens with 32 heads of 128 (relative norm): 1.6e-7 to 9.1e-7, now 1.2e-7 to 1.4e-7, in the
+// same time (235 us, 236 us).  A tile's Gammas stand between it and the one before: the sum and
+// the product are scanned side by side, and 1 / Gamma is taken by the reciprocal (a division:
+// 2 heads of 32 18.1 us for 17.1, 16K tokens of 32 heads of 32 298 us for 272).
 //
 // The tokens of a segment follow one another, so one segment per sequence would
 // leave most SMs without work.  The sequence is cut into segments (find_seg): a
@@ -103,13 +105,11 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // e^x - 1 for |x| < kNearOne: its Taylor series, cut off below 2^-29 of the sum
 __device__ __forceinline__ float near_expm1(float x) {
-    float q = 1.f / 5040.f;
-    q = fmaf(q, x, 1.f / 720.f);
-    q = fmaf(q, x, 1.f / 120.f);
-    q = fmaf(q, x, 1.f / 24.f);
-    q = fmaf(q, x, 1.f / 6.f);
-    q = fmaf(q, x, 0.5f);
-    return fmaf(x * x, q, x);
+    const float x2 = x * x;
+    float hi = fmaf(1.f / 5040.f, x, 1.f / 720.f);
+    hi = fmaf(hi, x2, fmaf(1.f / 120.f, x, 1.f / 24.f));
+    const float lo = fmaf(1.f / 6.f, x, 0.5f);
+    return fmaf(x2, fmaf(hi, x2, lo), x);
 }
 
 // ROWS state rows per thread: 8 (4 where a warp of 8 would have more rows than the head), or
@@ -149,8 +149,12 @@ struct alignas(16) Tile {
 };
 
 // READ: the second pass (start states, read-out, final state); otherwise the first
+// CTAs per SM: 8 rows fill 128 registers and still gain from a fourth CTA (3: 240 -> 252 us for
+// the layer); 4 and 2 rows come where there are fewer CTAs, and spills cost more than another
+// CTA gains (4 rows, 16 x 300 tokens of 64 heads of 32: 7 CTAs 107 us, 5 82 us; 2 rows, 4096
+// tokens of 64 heads of 32: 8 CTAs 158 us, 7 145 us, 5 158 us)
 template <int DK, int ROWS, typename T, bool READ>
-__global__ void __launch_bounds__(128, ROWS == 8 ? 4 : ROWS == 4 ? 7 : 8)
+__global__ void __launch_bounds__(128, ROWS == 8 ? 4 : ROWS == 4 ? 5 : 7)
 scan_rows_kernel(const RowParams p) {
     constexpr int LPR = DK / kCols;          // lanes per row group
     constexpr int RPW = rows_per_warp<DK, ROWS>();
@@ -235,14 +239,13 @@ scan_rows_kernel(const RowParams p) {
                 }
                 if (!READ) run += (double)__shfl_sync(0xffffffffu, sum, kTile - 1);
                 const float lg = sum + left, less = near_expm1(lg);
-                const bool near = __all_sync(0xffffffffu, lane >= kTile || fabsf(lg) < kNearOne);
+                const bool near = fabsf(lg) < kNearOne;
                 gamma = near ? 1.f + less : gamma;
-                // what 1 + less was rounded by (exact, |less| < 1); 1 / gamma is near enough 1 - less
-                const float lost = ((1.f - gamma) + less) * (1.f - less);
-                left = near ? __shfl_sync(0xffffffffu, lost, kTile - 1) : 0.f;
                 const float total = __shfl_sync(0xffffffffu, gamma, kTile - 1);
+                // what 1 + less was rounded by (exact, |less| < 1); 1 / gamma is near enough 1 - less
+                left = __shfl_sync(0xffffffffu, near ? ((1.f - gamma) + less) * (1.f - less) : 0.f, kTile - 1);
                 const bool mild = total >= kMildTile;
-                const float2 step = mild ? make_float2(dl / gamma, gamma) : make_float2(dl, al);
+                const float2 step = mild ? make_float2(dl * __frcp_rn(gamma), gamma) : make_float2(dl, al);
                 if (lane < kTile) t.step[lane] = step;
                 if (lane == 0) t.total = mild ? total : 0.f;
             }
