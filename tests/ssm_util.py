@@ -50,9 +50,8 @@ def within(out, ref, allow, what):
 def check_scan(y, hT, ref, dtype, tensor_cores, what=""):
     """Bounds: the result's own rounding, the fp32 roundings on the way (doubled, for sums
     in another order and the hardware exponential), and on the tensor-core path three bf16
-    roundings of each term of y: a term inside its chunk has one (its decayed score), one
-    from before it three (its weight, the weighted value, the state), and with u = 2^-8
-    (1 + u)^3 - 1 = 3 u (1 + u + u^2 / 3) <= 3 u (1 + 2^-6)."""
+    roundings of each term of y, more than any has (term_bounds counts them term by term):
+    with u = 2^-8, (1 + u)^3 - 1 = 3 u (1 + u + u^2 / 3) <= 3 u (1 + 2^-6)."""
     r_y, r_h, y_abs, y_units, h_units = ref
     u = U[dtype]
     allow = u * np.abs(r_y) + 2 * U32 * (1 + u) * y_units
